@@ -254,6 +254,145 @@ dsa_status dsa_mx_quantize(const dsa_bf16 *x, int64_t rows, int cols, int fmt,
                            uint8_t *codes, uint8_t *scales, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Grouped-query layers over a paged key/value cache: appending rotated keys
+ * and values, selecting pages by a cheap score, attention over all or the
+ * selected pages.  The pages describe the token-level selection of one
+ * sequence; these calls give its page-level counterpart ([IDX] §5.2 selects
+ * blocks of m tokens, §5.4 scores with 8-bit operands) over the cache that a
+ * serving engine keeps.
+ *
+ * The cache is a pool of n_pages pages of `page` consecutive tokens, laid out
+ * [n_pages, n_kv, page, D] for K and for V.
+ *   DSA_KV_BF16: bf16 values; k_scale and v_scale are NULL.
+ *   DSA_KV_E4M3: 8-bit E4M3 codes with one f32 scale for each page and head,
+ *     k_scale and v_scale [n_pages, n_kv]; value = code * scale.  Attention
+ *     takes any positive finite scales; dsa_paged_append writes powers of two.
+ *   sum [n_pages, n_kv, D] int8 and sum_scale [n_pages, n_kv] f32 hold one
+ *     summary for each COMPLETE page: sum * sum_scale is the mean of the
+ *     page's cached keys rounded to whole steps of amax / 127.  Both NULL when
+ *     no page selection is used.
+ * Supported: page in {16, 32, 64, 128}; D in {64, 128}; n_pages * n_kv < 2^31.
+ *
+ * A batch holds B sequences with packed rows as in dsa_varlen: rows cu_q[b] ..
+ * cu_q[b+1]-1 belong to sequence b, and row i of it is the token at position
+ * start_pos[b] + i.  block_table [B, max_pages] names the pool page of each
+ * page of a sequence: positions j * page .. j * page + page - 1 of sequence b
+ * are in block_table[b * max_pages + j].  cu_q, start_pos and block_table are
+ * DEVICE int32 arrays; total_q = cu_q[B] and the bounds max_Lq >= every row
+ * count and max_Lk >= every start_pos[b] + rows size the launches.
+ *
+ * Contract, checked on the device by dsa_check_paged: cu_q starts at 0, never
+ * decreases and ends at total_q; start_pos[b] >= 0; the bounds hold; the table
+ * entries of the pages that hold positions below start_pos[b] + rows name
+ * pages of the pool.  A batch that breaks it gets unspecified rows but no
+ * access outside the tensors.  Several sequences may share a page that is only
+ * read; a page that a call appends to belongs to one sequence.
+ *
+ * Visibility: row i at t = start_pos[b] + i sees s < t as everywhere in this
+ * library, or s <= t when `inclusive` is 1 (its own token, which has then been
+ * appended).  Slots that a row does not see may hold anything, NaN included. */
+#define DSA_KV_BF16 0
+#define DSA_KV_E4M3 1
+typedef struct {
+  int n_pages, page, n_kv, D, fmt;
+  void *k, *v;              /* [n_pages, n_kv, page, D] bf16 or E4M3 codes */
+  float *k_scale, *v_scale; /* [n_pages, n_kv], E4M3 only */
+  int8_t *sum;              /* [n_pages, n_kv, D] or NULL */
+  float *sum_scale;         /* [n_pages, n_kv] or NULL */
+} dsa_paged_kv;
+
+typedef struct {
+  int B;                      /* sequences */
+  const int32_t *cu_q;        /* device [B + 1] row offsets */
+  const int32_t *start_pos;   /* device [B] position of each sequence's first row */
+  const int32_t *block_table; /* device [B, max_pages] */
+  int max_pages;              /* entries of a block table row */
+  int total_q;                /* cu_q[B] */
+  int max_Lq, max_Lk;         /* bounds of the rows and of start_pos + rows */
+} dsa_paged_batch;
+
+/* Appends keys and values to the cache and rotates keys and queries by their
+ * positions on the way.
+ *   k, v: rows of [n_kv, D] bf16 at k + r * k_row_stride (elements; a multiple
+ *     of 8, at least n_kv * D), r < total_q: a slice of a fused projection may
+ *     be passed as it is.
+ *   cos, sin [n_pos, rot / 2] f32: the angles of each position (row = absolute
+ *     position; max_Lk <= n_pos).  rot = 0: no rotation, cos and sin NULL.
+ *     The first rot columns of a head rotate, in pairs (i, i + rot/2), or
+ *     (2i, 2i + 1) when `interleaved` is 1:
+ *       (a, b) -> (a cos - b sin, b cos + a sin),
+ *     each product and sum rounded to f32.  rot is a multiple of 16, <= D.
+ *   q (rows of [n_h, D] at q + r * q_row_stride), q_out [total_q, n_h, D]
+ *     bf16 (written): the rotated queries; both NULL to leave them out.
+ *     q_out may be q itself when q is contiguous.
+ * bf16 caches hold the rotated keys and the values rounded once.  E4M3 caches:
+ * for each page and head that receives tokens, the scale becomes X = the
+ * smallest power of two (at least 2^-100) with amax <= 448 X over the finite
+ * new values, and not less than the old scale when the page already holds
+ * tokens of this sequence (its first new slot is not slot 0); new codes are
+ * x / X rounded to nearest even (infinities saturate to +-448, NaN stays NaN)
+ * and older codes are rescaled to the new X the same way.  What was in a page
+ * before its slot 0 is written is forgotten.
+ * Summaries (when kv->sum is given) are written for the pages that this call
+ * completes, from the cached (rounded) keys: their sum over the slots by
+ * halving (slot i + slot i + page/2, ...) in f32, codes rint(sum * (127 /
+ * amax)), scale (amax / 127) / page; a page whose sum is not finite, or
+ * below 3.8e-37 everywhere, gets zeros. */
+dsa_status dsa_paged_append(const dsa_paged_kv *kv, const dsa_paged_batch *batch,
+                            const dsa_bf16 *k, int64_t k_row_stride, const dsa_bf16 *v,
+                            int64_t v_row_stride, const float *cos, const float *sin,
+                            int n_pos, int rot, int interleaved, const dsa_bf16 *q,
+                            int64_t q_row_stride, int n_h, dsa_bf16 *q_out, void *stream);
+
+/* Page selection: for each row and key/value head, the n_sel pages of the row's
+ * sequence that score best, among the n = ceil(visible positions / page) pages
+ * the row sees.  q [total_q, n_h, D] bf16, n_h a multiple of n_kv.  With the
+ * head group's pooled query qs = sum of its n_h / n_kv query heads (formed
+ * exactly and rounded to f32), c = rint(qs * (127 / amax qs)):
+ *   score(p) = f32(sum_d c[d] * sum[p, d]) * sum_scale[p].
+ * The dot is a whole number below 2^24, so the score is the same however it
+ * is computed.  The first n_first and the last n_last pages that the row sees
+ * are always selected (n_last >= 1: the last page may be incomplete and has no
+ * summary then; n_first + n_last <= n_sel).  Output sel [total_q, n_kv, n_sel]
+ * int32: page numbers within the sequence, ascending, then -1; equal scores
+ * prefer the lower page; all pages when n <= n_sel.  A row that sees nothing
+ * gets -1.  A pooled query that is not finite, or
+ * below 3.8e-37 everywhere, scores 0 on every page.
+ * Supported: n_sel <= 1024, n_h / n_kv <= 128, ceil(max_Lk / page) <= 49152. */
+dsa_status dsa_page_topk(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
+                         const dsa_paged_batch *batch, int inclusive, int n_sel,
+                         int n_first, int n_last, int32_t *sel, void *stream);
+
+/* Attention over the cache.  Query head h reads key/value head h / (n_h/n_kv):
+ *   e_s = scale * q[t,h,:] . K[s],  out[t,h,:] = sum_s softmax_s(e) V[s],
+ *   lse[t,h] = log sum_s exp(e_s)   (natural log)
+ * over the visible positions s of the row: all of them (sel NULL), or those in
+ * the pages that sel [total_q, n_kv, n_sel] names for the row and key/value
+ * head (page numbers within the sequence in any order, no page twice; entries
+ * outside the row's visible pages are skipped, as -1 is).  A row that sees
+ * nothing gets out = 0 and lse = -inf.
+ * Numerics: scores are f32 sums of exact products; the softmax runs in f32;
+ * the weights enter the P.V product with 8 significant bits (bf16, or two
+ * E4M3 terms for an 8-bit cache), accumulated in f32; out is rounded once.
+ *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written); lse
+ *   [total_q, n_h] f32 (written; may be NULL).
+ * Supported: n_h a multiple of n_kv, n_h <= 128; n_sel <= 1024.
+ * Workspace: dsa_paged_attn_workspace() bytes, contents undefined on entry; a
+ * call in flight needs a workspace of its own. */
+size_t dsa_paged_attn_workspace(const dsa_paged_kv *kv, const dsa_paged_batch *batch,
+                                int n_h, int n_sel);
+dsa_status dsa_paged_attn(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
+                          const dsa_paged_batch *batch, int inclusive, const int32_t *sel,
+                          int n_sel, float scale, dsa_bf16 *out, float *lse, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Checks the contract of a paged batch on the device and writes the number of
+ * sequences that break it to *bad_seqs (one device int, overwritten; read it
+ * after the stream completes).  Allocates nothing. */
+dsa_status dsa_check_paged(const dsa_paged_kv *kv, const dsa_paged_batch *batch, int *bad_seqs,
+                           void *stream);
+
+/* ---------------------------------------------------------------------------
  * Allocation-free variant of dsa_indexer_topk.  The pages describe no such
  * entry point; it exists for callers that cannot provide device memory on
  * demand -- an engine whose allocator already owns all of HBM, a C program

@@ -1,0 +1,534 @@
+// paged.cu -- the paged key/value cache (include/dsa.h, dsa_paged_kv): host
+// checks, the append kernel (rotation, 8-bit quantisation with a scale for
+// each page and head, page summaries) and the page selection.
+#include <algorithm>
+#include <string>
+
+#include "paged.cuh"
+
+namespace dsa {
+
+dsa_status check_paged_host(const char* who, const dsa_paged_kv* kv, const dsa_paged_batch* pb, PagedArgs* out) {
+  const auto bad = [&](dsa_status st, const char* what) { return set_error(st, std::string(who) + ": " + what); };
+  if (!kv || !pb) return bad(DSA_ERR_INVALID_ARG, "null cache or batch descriptor");
+  if (!kv->k || !kv->v || !pb->cu_q || !pb->start_pos || !pb->block_table)
+    return bad(DSA_ERR_INVALID_ARG, "null pointer in a descriptor");
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !aligned16(kv->k_scale) || !aligned16(kv->v_scale) ||
+      !aligned16(kv->sum) || !aligned16(kv->sum_scale))
+    return bad(DSA_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(pb->cu_q) | reinterpret_cast<uintptr_t>(pb->start_pos) |
+       reinterpret_cast<uintptr_t>(pb->block_table)) & 3u)
+    return bad(DSA_ERR_INVALID_ARG, "batch arrays must be 4-byte aligned");
+  if (kv->n_pages < 1 || kv->n_kv < 1 || pb->B < 1 || pb->max_pages < 1 || pb->total_q < 1 || pb->max_Lq < 1 ||
+      pb->max_Lk < 1)
+    return bad(DSA_ERR_INVALID_ARG, "sizes must be positive");
+  if (kv->page != 16 && kv->page != 32 && kv->page != 64 && kv->page != 128)
+    return bad(DSA_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 tokens");
+  if (kv->D != 64 && kv->D != 128) return bad(DSA_ERR_UNSUPPORTED, "D must be 64 or 128");
+  if (kv->fmt != DSA_KV_BF16 && kv->fmt != DSA_KV_E4M3) return bad(DSA_ERR_UNSUPPORTED, "unknown cache format");
+  if (kv->fmt == DSA_KV_E4M3 ? (!kv->k_scale || !kv->v_scale) : (kv->k_scale || kv->v_scale))
+    return bad(DSA_ERR_INVALID_ARG, "an E4M3 cache needs both scales and a bf16 cache takes none");
+  if (!kv->sum != !kv->sum_scale) return bad(DSA_ERR_INVALID_ARG, "summaries need both arrays");
+  if (static_cast<long long>(kv->n_pages) * kv->n_kv > (1ll << 31) - 1 || kv->n_kv > 128)
+    return bad(DSA_ERR_UNSUPPORTED, "too many pages or heads");
+  if (pb->max_Lq > pb->total_q) return bad(DSA_ERR_INVALID_ARG, "max_Lq exceeds total_q");
+  if (pb->max_Lk > (1 << 30)) return bad(DSA_ERR_UNSUPPORTED, "max_Lk too large");
+  if (static_cast<long long>(pb->max_pages) * kv->page < pb->max_Lk)
+    return bad(DSA_ERR_INVALID_ARG, "the block table does not cover max_Lk positions");
+  if (out)
+    *out = PagedArgs{kv->k, kv->v, kv->k_scale, kv->v_scale, kv->sum, kv->sum_scale, kv->n_pages, kv->n_kv,
+                     pb->cu_q, pb->start_pos, pb->block_table, pb->B, pb->max_pages, pb->total_q, pb->max_Lq, pb->max_Lk};
+  return DSA_OK;
+}
+
+namespace {
+
+// ---------------------------------------------------------------- contract
+__global__ void check_paged_kernel(const PagedArgs a, int page, int* bad) {
+  const int b = blockIdx.x;
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], sp = a.sp[b];
+  const long long end = static_cast<long long>(sp) + q1 - q0;
+  bool ok = q1 >= q0 && q1 - q0 <= a.max_Lq && sp >= 0 && end <= a.max_Lk;
+  if (b == 0) ok = ok && q0 == 0;
+  if (b == a.B - 1) ok = ok && q1 == a.total_q;
+  if (ok)
+    for (long long j = threadIdx.x; j * page < end; j += blockDim.x) ok = ok && paged_page(a, b, static_cast<int>(j)) >= 0;
+  if (__syncthreads_or(!ok) && threadIdx.x == 0) atomicAdd(bad, 1);
+}
+
+// ---------------------------------------------------------------- append
+struct AppendParams {
+  PagedArgs a;
+  const dsa_bf16 *k, *v, *q;
+  dsa_bf16* q_out;
+  int64_t k_stride, v_stride, q_stride;
+  const float *cos, *sin;
+  int n_h, half, interleaved, n_pos;
+  int touched;     // pages a sequence can touch
+  int64_t units;   // blocks of cache pages; the blocks after them rotate q
+};
+
+constexpr int kAppendThreads = 256;
+constexpr float kMaxF32 = 3.402823466e38f;
+constexpr float kMinTop = 3.8e-37f;  // 127 / amax stays finite above it
+
+// Eight consecutive columns (from column c) of a head's row x, rotated by the
+// angles of position pos.  Products and sums are rounded one by one (no fused
+// multiply-add), so that the result does not depend on the compiler.
+__device__ __forceinline__ void rotated8(const dsa_bf16* x, int c, int pos, const AppendParams& p, float (&f)[8]) {
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(x + c), f);
+  if (c >= 2 * p.half) return;
+  const int64_t at = static_cast<int64_t>(pos) * p.half;
+  if (p.interleaved) {
+    const float4 cs = __ldg(reinterpret_cast<const float4*>(p.cos + at + c / 2));
+    const float4 sn = __ldg(reinterpret_cast<const float4*>(p.sin + at + c / 2));
+    const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = f[2 * i], w = f[2 * i + 1];
+      f[2 * i] = __fsub_rn(__fmul_rn(u, cc[i]), __fmul_rn(w, ss[i]));
+      f[2 * i + 1] = __fadd_rn(__fmul_rn(w, cc[i]), __fmul_rn(u, ss[i]));
+    }
+    return;
+  }
+  const bool low = c < p.half;
+  const int pair = low ? c : c - p.half;
+  float o[8];
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(x + (low ? c + p.half : pair)), o);
+  const float4* cs4 = reinterpret_cast<const float4*>(p.cos + at + pair);
+  const float4* sn4 = reinterpret_cast<const float4*>(p.sin + at + pair);
+  const float4 c0 = __ldg(cs4), c1 = __ldg(cs4 + 1), s0 = __ldg(sn4), s1 = __ldg(sn4 + 1);
+  const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    f[i] = low ? __fsub_rn(__fmul_rn(f[i], cc[i]), __fmul_rn(o[i], ss[i]))
+               : __fadd_rn(__fmul_rn(f[i], cc[i]), __fmul_rn(o[i], ss[i]));
+}
+
+// Smallest power of two X with amax <= 448 X (448 = 1.75 * 2^8), at least 2^-100.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(max(e, -100) + 127) << 23);
+}
+
+// Reduces a maximum over the block (all threads get it).
+__device__ __forceinline__ float block_max(float x, float* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = red[0];
+#pragma unroll
+  for (int i = 1; i < kAppendThreads / 32; ++i) x = fmaxf(x, red[i]);
+  return x;
+}
+
+// One block per (sequence, touched page, head, K or V): every slot of that
+// page and head has one owner, so the scale, the rescaled older codes and the
+// summary need no atomics and no second pass over the new rows.  A thread owns
+// 8 columns of every (256 / (D/8))-th slot, in registers from the load to the
+// store.  Bound by memory: new rows in, cache rows out, each once.
+template <int D, int PAGE, bool F8>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
+  constexpr int kVecs = D / 8;                    // threads per slot
+  constexpr int kRows = kAppendThreads / kVecs;   // slots per step
+  constexpr int kSteps = PAGE > kRows ? PAGE / kRows : 1;
+  __shared__ float red[kAppendThreads / 32];
+  __shared__ float part[kAppendThreads][9];
+  pdl_trigger();
+  pdl_wait();
+  const int vec = threadIdx.x % kVecs, g = threadIdx.x / kVecs, c = vec * 8;
+
+  if (blockIdx.x >= p.units) {  // queries: 8 columns of a head per thread
+    const int per_row = p.n_h * kVecs;
+    const int64_t n = static_cast<int64_t>(p.a.total_q) * per_row;
+    const int lane = threadIdx.x & 31;
+    for (int64_t e0 = (blockIdx.x - p.units) * kAppendThreads + (threadIdx.x - lane); e0 < n;
+         e0 += static_cast<int64_t>(gridDim.x - p.units) * kAppendThreads) {
+      const int64_t e = min(e0 + lane, n - 1);
+      const int row = static_cast<int>(e / per_row), in = static_cast<int>(e % per_row);
+      const int b = paged_seq(p.a, row);
+      const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - __ldg(p.a.cu_q + b);
+      const bool ok = e0 + lane < n && (!p.half || (pos >= 0 && pos < p.n_pos));
+      float f[8];
+      if (ok) rotated8(p.q + row * p.q_stride + (in / kVecs) * D, (in % kVecs) * 8, static_cast<int>(pos), p, f);
+      __syncwarp();  // q_out may be q: a head's columns are all read before any is written
+      if (ok)
+        *reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(row) * p.n_h + in / kVecs) * D + (in % kVecs) * 8) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+    return;
+  }
+
+  int u = static_cast<int>(blockIdx.x);
+  const bool is_v = u & 1;
+  u >>= 1;
+  const int head = u % p.a.n_kv;
+  u /= p.a.n_kv;
+  const int tp = u % p.touched, b = u / p.touched;
+  int r0, n;
+  paged_rows(p.a, b, r0, n);
+  const int sp = __ldg(p.a.sp + b);
+  if (n == 0 || sp < 0 || static_cast<long long>(sp) + n > p.a.max_Lk) return;
+  const int j = sp / PAGE + tp;              // page of the sequence
+  const int first = max(sp, j * PAGE), end = min(sp + n, (j + 1) * PAGE);
+  if (first >= end) return;
+  const int pg = paged_page(p.a, b, j);
+  if (pg < 0) return;
+  const int a0 = first - j * PAGE, a1 = end - j * PAGE;  // new slots of the page
+  const bool whole = !is_v && a1 == PAGE && p.a.sum;
+  const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
+  const int64_t base = unit * PAGE * D;
+
+  float f[kSteps][8];
+  float amax = 0.f;
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int slot = s * kRows + g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[s][i] = 0.f;
+    if (slot >= a0 && slot < a1) {
+      const int pos = j * PAGE + slot;
+      const int64_t row = r0 + (pos - sp);
+      if (is_v) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + head * D + c)), f[s]);
+      else rotated8(p.k + row * p.k_stride + head * D, c, pos, p, f[s]);
+      if constexpr (F8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[s][i]) <= kMaxF32 ? fabsf(f[s][i]) : 0.f);
+      }
+    }
+  }
+
+  float scale = 1.f, ratio = 1.f;
+  if constexpr (F8) {
+    float* sc = (is_v ? p.a.v_scale : p.a.k_scale) + unit;
+    scale = pow2_scale(block_max(amax, red));
+    if (a0 > 0) {
+      const float old = *sc;
+      scale = fmaxf(scale, old);
+      ratio = __fdiv_rn(old, scale);
+    }
+    __syncthreads();  // every thread has read the old scale
+    if (threadIdx.x == 0) *sc = scale;
+  }
+
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int slot = s * kRows + g;
+    const bool fresh = slot >= a0 && slot < a1, older = slot < a0 && (whole || ratio != 1.f);
+    if (!fresh && !older) continue;
+    const int64_t at = base + static_cast<int64_t>(slot) * D + c;
+    if constexpr (F8) {
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? p.a.v : p.a.k) + at);
+      float mul = ratio;
+      if (older) {
+        const uint2 w = *dst;
+        const uint32_t h[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = e4m3x2_to_f32(h[i]);
+          f[s][2 * i] = x.x;
+          f[s][2 * i + 1] = x.y;
+        }
+      } else {
+        mul = __fdiv_rn(1.f, scale);  // a power of two: exact (at most 2^100)
+      }
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[i] = e4m3x2(f[s][2 * i] * mul, f[s][2 * i + 1] * mul);
+        const float2 x = e4m3x2_to_f32(h[i]);
+        f[s][2 * i] = x.x;  // the summary takes what the cache holds
+        f[s][2 * i + 1] = x.y;
+      }
+      if (fresh || ratio != 1.f) *dst = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<dsa_bf16*>(is_v ? p.a.v : p.a.k) + at);
+      uint4 w;
+      if (older) w = *dst;
+      else {
+        w = make_uint4(pack_bf16(f[s][0], f[s][1]), pack_bf16(f[s][2], f[s][3]), pack_bf16(f[s][4], f[s][5]),
+                       pack_bf16(f[s][6], f[s][7]));
+        *dst = w;
+      }
+      bf16x8_to_f32(w, f[s]);
+    }
+  }
+  if (!whole) return;
+
+  // ---- summary of a page that is now complete: the sum over its slots by
+  // halving (slot i + slot i + PAGE/2, ...).  The slots of a thread are g,
+  // g + kRows, ...: the first levels are its own, the rest go through shared
+  // memory in the same order.
+#pragma unroll
+  for (int h = kSteps / 2; h; h >>= 1)
+#pragma unroll
+    for (int s = 0; s < kSteps / 2; ++s)
+      if (s < h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[s][i] = __fadd_rn(f[s][i], f[s + h][i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = f[0][i];
+  __syncthreads();
+  constexpr int kGroups = PAGE < kRows ? PAGE : kRows;
+  for (int h = kGroups / 2; h; h >>= 1) {
+    if (g < h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = __fadd_rn(part[threadIdx.x][i], part[threadIdx.x + h * kVecs][i]);
+    __syncthreads();
+  }
+  float top = 0.f;
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = __fmul_rn(part[vec][i], scale);
+    f[0][i] = x;
+    fine = fine && fabsf(x) <= kMaxF32;
+    top = fmaxf(top, fabsf(x));
+  }
+  fine = __syncthreads_and(fine);
+  top = block_max(top, red);
+  fine = fine && top >= kMinTop;
+  if (g == 0) {
+    const float inv = __fdiv_rn(127.f, top);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int code = fine ? __float2int_rn(__fmul_rn(f[0][i], inv)) : 0;
+      w[i >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (i & 3));
+    }
+    *reinterpret_cast<uint2*>(p.a.sum + unit * D + c) = make_uint2(w[0], w[1]);
+    if (vec == 0) p.a.sum_scale[unit] = fine ? __fmul_rn(__fdiv_rn(top, 127.f), 1.f / PAGE) : 0.f;
+  }
+}
+
+template <int D, int PAGE>
+cudaError_t launch_append(const AppendParams& p, bool f8, unsigned grid, cudaStream_t s) {
+  return f8 ? launch_pdl(paged_append_kernel<D, PAGE, true>, dim3(grid), dim3(kAppendThreads), 0, s, p)
+            : launch_pdl(paged_append_kernel<D, PAGE, false>, dim3(grid), dim3(kAppendThreads), 0, s, p);
+}
+template <int D>
+cudaError_t launch_append(const AppendParams& p, int page, bool f8, unsigned grid, cudaStream_t s) {
+  switch (page) {
+    case 16: return launch_append<D, 16>(p, f8, grid, s);
+    case 32: return launch_append<D, 32>(p, f8, grid, s);
+    case 64: return launch_append<D, 64>(p, f8, grid, s);
+    default: return launch_append<D, 128>(p, f8, grid, s);
+  }
+}
+
+// ---------------------------------------------------------------- selection
+constexpr int kSelThreads = 256;
+constexpr int kSelMaxPages = 49152;  // one f32 key per visible page in shared memory
+
+struct SelParams {
+  PagedArgs a;
+  const dsa_bf16* q;
+  int n_h, page, inclusive, n_sel, n_first, n_last;
+  int32_t* sel;
+};
+
+// One block per (row, head): pooled query codes, one score key per visible
+// page in shared memory, an 8-bit radix select of the n_sel-th largest key
+// and an ordered scan that writes the pages above it (ties: lowest first).
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ __align__(16) int8_t qc[D];
+  __shared__ float red[kSelThreads / 32];
+  __shared__ int hist[256], scan[kSelThreads / 32], pick[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int row = blockIdx.x / p.a.n_kv, head = blockIdx.x % p.a.n_kv;
+  const int b = paged_seq(p.a, row);
+  const int t = paged_visible(p.a, b, row - __ldg(p.a.cu_q + b), p.inclusive);
+  const int n = (t + p.page - 1) / p.page;
+  int32_t* out = p.sel + (static_cast<int64_t>(row) * p.a.n_kv + head) * p.n_sel;
+  if (n <= p.n_sel) {
+    for (int e = tid; e < p.n_sel; e += kSelThreads) out[e] = e < n ? e : -1;
+    return;
+  }
+  // pooled query: the exact sum over the group, rounded once
+  const int G = p.n_h / p.a.n_kv;
+  float qs = 0.f;
+  if (tid < D) {
+    const dsa_bf16* x = p.q + (static_cast<int64_t>(row) * p.n_h + head * G) * D + tid;
+    double acc = 0.0;
+    for (int h = 0; h < G; ++h) acc += static_cast<double>(__uint_as_float(static_cast<uint32_t>(__ldg(x + h * D)) << 16));
+    qs = static_cast<float>(acc);
+  }
+  const bool fine = __syncthreads_and(fabsf(qs) <= kMaxF32);
+  const float amax = block_max(fabsf(qs), red);
+  if (tid < D) qc[tid] = fine && amax >= kMinTop ? static_cast<int8_t>(__float2int_rn(__fmul_rn(qs, __fdiv_rn(127.f, amax)))) : 0;
+  __syncthreads();
+  for (int j = tid; j < n; j += kSelThreads) {
+    uint32_t key = 0xffffffffu;
+    if (j >= p.n_first && j < n - p.n_last) {
+      const int pg = paged_page(p.a, b, j);
+      key = 0u;
+      if (pg >= 0) {
+        const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
+        const int4* s4 = reinterpret_cast<const int4*>(p.a.sum + unit * D);
+        int dot = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int4 w = __ldg(s4 + i);
+          const int4 x = *reinterpret_cast<const int4*>(qc + 16 * i);
+          dot = __dp4a(w.x, x.x, __dp4a(w.y, x.y, __dp4a(w.z, x.z, __dp4a(w.w, x.w, dot))));
+        }
+        key = float_key(__fmul_rn(static_cast<float>(dot), __ldg(p.a.sum_scale + unit)));
+      }
+    }
+    keys[j] = key;
+  }
+  // ---- the n_sel-th largest key
+  uint32_t prefix = 0;
+  int want = p.n_sel;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    hist[tid] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSelThreads)
+      if (shift == 24 || (keys[j] >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
+    __syncthreads();
+    if (warp == 0) {  // bins from the top, 8 per lane
+      int s = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += hist[255 - (lane * 8 + i)];
+      int incl = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int above = incl - s;
+      if (above < want && incl >= want) {
+        int i = 0;
+        for (; above + hist[255 - (lane * 8 + i)] < want; ++i) above += hist[255 - (lane * 8 + i)];
+        pick[0] = 255 - (lane * 8 + i);
+        pick[1] = want - above;
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(pick[0]) << shift;
+    want = pick[1];
+  }
+  // ---- ordered output: keys above the threshold, and the first `want` equal to it
+  int at = 0, ties = 0;
+  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const uint32_t key = j < n ? keys[j] : 0u;
+    const bool gt = j < n && key > prefix, eq = j < n && key == prefix;
+    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    __syncthreads();
+    if (lane == 0) scan[warp] = __popc(bg) | (__popc(be) << 16);
+    __syncthreads();
+    int g0 = at, e0 = ties, gsum = 0, esum = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      const int c = scan[w];
+      if (w < warp) { g0 += c & 0xffff; e0 += c >> 16; }
+      gsum += c & 0xffff;
+      esum += c >> 16;
+    }
+    const unsigned lt = (1u << lane) - 1u;
+    g0 += __popc(bg & lt);
+    e0 += __popc(be & lt);
+    if (gt) out[g0 + min(e0, want)] = j;
+    else if (eq && e0 < want) out[g0 + e0] = j;
+    at += gsum;
+    ties += esum;
+  }
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" {
+
+dsa_status dsa_paged_append(const dsa_paged_kv* kv, const dsa_paged_batch* batch, const dsa_bf16* k,
+                            int64_t k_row_stride, const dsa_bf16* v, int64_t v_row_stride, const float* cos,
+                            const float* sin, int n_pos, int rot, int interleaved, const dsa_bf16* q,
+                            int64_t q_row_stride, int n_h, dsa_bf16* q_out, void* stream) {
+  AppendParams p{};
+  dsa_status st = check_paged_host("dsa_paged_append", kv, batch, &p.a);
+  if (st != DSA_OK) return st;
+  if (!k || !v || !q != !q_out) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: null pointer");
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(cos) || !aligned16(sin))
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: pointers must be 16-byte aligned");
+  const int64_t need = static_cast<int64_t>(kv->n_kv) * kv->D;
+  if (k_row_stride < need || v_row_stride < need || (k_row_stride % 8) || (v_row_stride % 8))
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: row strides must cover the heads and be multiples of 8");
+  if (q && (n_h < 1 || q_row_stride < static_cast<int64_t>(n_h) * kv->D || (q_row_stride % 8)))
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: bad n_h or query row stride");
+  if (q && n_h > 1024) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: n_h too large");
+  if (q == q_out && q && q_row_stride != static_cast<int64_t>(n_h) * kv->D)
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: in-place queries must be contiguous");
+  if (rot < 0 || rot > kv->D || rot % 16) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: rot must be a multiple of 16, at most D");
+  if (interleaved != 0 && interleaved != 1) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: interleaved is 0 or 1");
+  if (rot && (!cos || !sin || n_pos < batch->max_Lk))
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_append: cos and sin must cover max_Lk positions");
+  p.k = k; p.v = v; p.q = q; p.q_out = q_out;
+  p.k_stride = k_row_stride; p.v_stride = v_row_stride; p.q_stride = q_row_stride;
+  p.cos = cos; p.sin = sin; p.n_h = n_h; p.half = rot / 2; p.interleaved = interleaved; p.n_pos = n_pos;
+  p.touched = (batch->max_Lq + kv->page - 2) / kv->page + 1;
+  p.units = 2ll * batch->B * p.touched * kv->n_kv;
+  const int64_t q_blocks = q ? (static_cast<int64_t>(batch->total_q) * n_h * (kv->D / 8) + kAppendThreads - 1) / kAppendThreads : 0;
+  const int64_t grid = p.units + std::min<int64_t>(q_blocks, 1 << 20);
+  if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: batch too large");
+  const cudaError_t e = kv->D == 64
+      ? launch_append<64>(p, kv->page, kv->fmt == DSA_KV_E4M3, static_cast<unsigned>(grid), static_cast<cudaStream_t>(stream))
+      : launch_append<128>(p, kv->page, kv->fmt == DSA_KV_E4M3, static_cast<unsigned>(grid), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_paged_append launch: ") + cudaGetErrorString(e));
+  return DSA_OK;
+}
+
+dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, const dsa_paged_batch* batch,
+                         int inclusive, int n_sel, int n_first, int n_last, int32_t* sel, void* stream) {
+  SelParams p{};
+  dsa_status st = check_paged_host("dsa_page_topk", kv, batch, &p.a);
+  if (st != DSA_OK) return st;
+  if (!q || !sel || !kv->sum) return set_error(DSA_ERR_INVALID_ARG, "dsa_page_topk: null pointer, or a cache without summaries");
+  if (!aligned16(q) || !aligned16(sel)) return set_error(DSA_ERR_INVALID_ARG, "dsa_page_topk: pointers must be 16-byte aligned");
+  if (n_h < 1 || n_h % kv->n_kv) return set_error(DSA_ERR_INVALID_ARG, "dsa_page_topk: n_h must be a multiple of n_kv");
+  if (n_h / kv->n_kv > 128) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: more than 128 query heads per key/value head");
+  if (inclusive != 0 && inclusive != 1) return set_error(DSA_ERR_INVALID_ARG, "dsa_page_topk: inclusive is 0 or 1");
+  if (n_sel < 1 || n_first < 0 || n_last < 1 || static_cast<long long>(n_first) + n_last > n_sel)
+    return set_error(DSA_ERR_INVALID_ARG, "dsa_page_topk: need n_first >= 0, n_last >= 1, n_first + n_last <= n_sel");
+  const int max_n = (batch->max_Lk + kv->page - 1) / kv->page;
+  if (n_sel > 1024 || max_n > kSelMaxPages)
+    return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: n_sel <= 1024 and at most 49152 pages per sequence");
+  const int64_t grid = static_cast<int64_t>(batch->total_q) * kv->n_kv;
+  if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
+  p.q = q; p.n_h = n_h; p.page = kv->page; p.inclusive = inclusive; p.n_sel = n_sel; p.n_first = n_first; p.n_last = n_last;
+  p.sel = sel;
+  const int smem = max_n * 4;
+  const void* fn = kv->D == 64 ? reinterpret_cast<const void*>(page_topk_kernel<64>) : reinterpret_cast<const void*>(page_topk_kernel<128>);
+  cudaError_t e = ensure_smem_limit(fn, smem);
+  if (e == cudaSuccess)
+    e = launch_pdl(kv->D == 64 ? page_topk_kernel<64> : page_topk_kernel<128>, dim3(static_cast<unsigned>(grid)), dim3(kSelThreads),
+                   smem, static_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_page_topk launch: ") + cudaGetErrorString(e));
+  return DSA_OK;
+}
+
+dsa_status dsa_check_paged(const dsa_paged_kv* kv, const dsa_paged_batch* batch, int* bad_seqs, void* stream) {
+  PagedArgs a{};
+  dsa_status st = check_paged_host("dsa_check_paged", kv, batch, &a);
+  if (st != DSA_OK) return st;
+  if (!bad_seqs) return set_error(DSA_ERR_INVALID_ARG, "dsa_check_paged: null pointer");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemsetAsync(bad_seqs, 0, sizeof(int), s);
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_check_paged: ") + cudaGetErrorString(e));
+  check_paged_kernel<<<static_cast<unsigned>(batch->B), 128, 0, s>>>(a, kv->page, bad_seqs);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_check_paged launch: ") + cudaGetErrorString(e));
+  return DSA_OK;
+}
+
+}  // extern "C"

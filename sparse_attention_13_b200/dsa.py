@@ -28,10 +28,12 @@ EXPORTS = ["dsa_last_error", "dsa_indexer_topk_workspace", "dsa_indexer_topk",
            "dsa_indexer_topk_varlen_workspace", "dsa_indexer_topk_varlen",
            "dsa_sparse_attn_varlen_workspace", "dsa_sparse_attn_varlen",
            "indexcache_forward_varlen_workspace", "indexcache_forward_varlen", "dsa_check_varlen",
-           "dsa_indexer_topk_lowprec_workspace", "dsa_indexer_topk_lowprec", "dsa_mx_quantize"]
+           "dsa_indexer_topk_lowprec_workspace", "dsa_indexer_topk_lowprec", "dsa_mx_quantize",
+           "dsa_paged_append", "dsa_page_topk", "dsa_paged_attn_workspace", "dsa_paged_attn", "dsa_check_paged"]
 
 DSA_FMT_E4M3, DSA_FMT_E2M1 = 0, 1
 FORMATS = {"e4m3": DSA_FMT_E4M3, "e2m1": DSA_FMT_E2M1}
+DSA_KV_BF16, DSA_KV_E4M3 = 0, 1
 
 
 class DSAError(RuntimeError):
@@ -57,6 +59,19 @@ class LayerIO(ctypes.Structure):
 class Varlen(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
                 ("start_pos", ctypes.c_void_p), ("total_q", ctypes.c_int), ("total_k", ctypes.c_int),
+                ("max_Lq", ctypes.c_int), ("max_Lk", ctypes.c_int)]
+
+
+class PagedKVDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int), ("page", ctypes.c_int), ("n_kv", ctypes.c_int), ("D", ctypes.c_int),
+                ("fmt", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("sum", ctypes.c_void_p),
+                ("sum_scale", ctypes.c_void_p)]
+
+
+class PagedBatchDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("start_pos", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int), ("total_q", ctypes.c_int),
                 ("max_Lq", ctypes.c_int), ("max_Lk", ctypes.c_int)]
 
 
@@ -133,6 +148,17 @@ def lib():
         L.dsa_indexer_topk_lowprec.restype = I
         L.dsa_mx_quantize.argtypes = [P, I64, I, I, P, P, P]
         L.dsa_mx_quantize.restype = I
+        KV, PB = ctypes.POINTER(PagedKVDesc), ctypes.POINTER(PagedBatchDesc)
+        L.dsa_paged_append.argtypes = [KV, PB, P, I64, P, I64, P, P, I, I, I, P, I64, I, P, P]
+        L.dsa_paged_append.restype = I
+        L.dsa_page_topk.argtypes = [P, I, KV, PB, I, I, I, I, P, P]
+        L.dsa_page_topk.restype = I
+        L.dsa_paged_attn_workspace.argtypes = [KV, PB, I, I]
+        L.dsa_paged_attn_workspace.restype = SZ
+        L.dsa_paged_attn.argtypes = [P, I, KV, PB, I, P, I, F32, P, P, P, SZ, P]
+        L.dsa_paged_attn.restype = I
+        L.dsa_check_paged.argtypes = [KV, PB, P, P]
+        L.dsa_check_paged.restype = I
         _lib = L
     return _lib
 
@@ -553,3 +579,235 @@ def mx_quantize(x, fmt: str):
     scales = torch.empty((rows, x.shape[-1] // 32), dtype=torch.uint8, device=x.device)
     _check(lib().dsa_mx_quantize(_ptr(x), rows, x.shape[-1], FORMATS[fmt], _ptr(codes), _ptr(scales), _stream(x)))
     return codes, scales
+
+
+# --------------------------------------------------------------------------
+# Grouped-query layers over a paged key/value cache (dsa_paged_kv and
+# dsa_paged_batch in include/dsa.h)
+class PagedKV:
+    """A pool of cache pages: k and v [n_pages, n_kv, page, D], bf16 or
+    float8_e4m3fn (then with k_scale and v_scale [n_pages, n_kv] f32), and
+    optionally the page summaries sum [n_pages, n_kv, D] int8 and sum_scale
+    [n_pages, n_kv] f32.  Holds the tensors; nothing is copied."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, sum=None, sum_scale=None):
+        import torch
+        _need(k, k.dtype, name="k")
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_kv, page, D]")
+        fmt = {torch.bfloat16: DSA_KV_BF16, torch.float8_e4m3fn: DSA_KV_E4M3}.get(k.dtype)
+        if fmt is None:
+            raise TypeError(f"k must be bfloat16 or float8_e4m3fn, got {k.dtype}")
+        _need(v, k.dtype, k.shape, "v")
+        n, h, page, D = k.shape
+        if (sum is None) != (sum_scale is None) or (fmt == DSA_KV_E4M3) != (k_scale is not None) or \
+                (k_scale is None) != (v_scale is None):
+            raise ValueError("an 8-bit cache needs k_scale and v_scale, a bf16 cache takes none; summaries need both arrays")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale), ("sum_scale", sum_scale)):
+            if t is not None:
+                _need(t, torch.float32, (n, h), name)
+        if sum is not None:
+            _need(sum, torch.int8, (n, h, D), "sum")
+        _same_device(k, v, k_scale, v_scale, sum, sum_scale)
+        self.k, self.v, self.k_scale, self.v_scale, self.sum, self.sum_scale = k, v, k_scale, v_scale, sum, sum_scale
+        self.desc = PagedKVDesc(n, page, h, D, fmt, *[None if t is None else t.data_ptr() for t in
+                                                      (k, v, k_scale, v_scale, sum, sum_scale)])
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_pages: int, page: int, n_kv: int, D: int, *, fmt: str = "e4m3", summaries: bool = True,
+              device="cuda"):
+        """A pool with undefined contents; fmt "bf16" or "e4m3"."""
+        import torch
+        if fmt not in ("bf16", "e4m3"):
+            raise ValueError('fmt must be "bf16" or "e4m3"')
+        dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        s = [new((n_pages, n_kv), torch.float32) for _ in range(2)] if fmt == "e4m3" else [None, None]
+        m = [new((n_pages, n_kv, D), torch.int8), new((n_pages, n_kv), torch.float32)] if summaries else [None, None]
+        return cls(new((n_pages, n_kv, page, D), dt), new((n_pages, n_kv, page, D), dt), *s, *m)
+
+
+class PagedBatch:
+    """A batch over a paged cache: cu_q [B + 1], start_pos [B] and block_table
+    [B, max_pages], int32 CUDA tensors, and the host sizes: total_q =
+    cu_q[B], bounds max_Lq of the rows and max_Lk of start_pos + rows of a
+    sequence.  Holds the tensors; their contents may change between calls as
+    long as the bounds hold."""
+
+    def __init__(self, cu_q, start_pos, block_table, *, total_q: int, max_Lq: int, max_Lk: int):
+        import torch
+        _need(block_table, torch.int32, name="block_table")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        B, max_pages = block_table.shape
+        _need(cu_q, torch.int32, (B + 1,), "cu_q")
+        _need(start_pos, torch.int32, (B,), "start_pos")
+        _same_device(block_table, cu_q, start_pos)
+        self.cu_q, self.start_pos, self.block_table = cu_q, start_pos, block_table
+        self.desc = PagedBatchDesc(B, cu_q.data_ptr(), start_pos.data_ptr(), block_table.data_ptr(), max_pages,
+                                   total_q, max_Lq, max_Lk)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def from_lens(cls, q_lens, start_pos, block_table):
+        """From host lists of row counts and first positions."""
+        import torch
+        cu = [0]
+        for n in q_lens:
+            cu.append(cu[-1] + int(n))
+        new = lambda x: torch.tensor(x, dtype=torch.int32, device=block_table.device)  # noqa: E731
+        return cls(new(cu), new([int(s) for s in start_pos]), block_table, total_q=cu[-1],
+                   max_Lq=max(max(map(int, q_lens)), 1),
+                   max_Lk=max(max(int(s) + int(n) for s, n in zip(start_pos, q_lens)), 1))
+
+    @property
+    def B(self):
+        return self.desc.B
+
+    @property
+    def total_q(self):
+        return self.desc.total_q
+
+
+def _same_device(*tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors are on different devices: {sorted(map(str, devs))}")
+
+
+class _on:
+    """Makes a tensor's device current for a call and gives its stream."""
+
+    def __init__(self, t):
+        self.dev = t.device
+
+    def __enter__(self):
+        import torch
+        self.old = torch.cuda.current_device()
+        if self.old != self.dev.index:
+            torch.cuda.set_device(self.dev)
+        return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+
+    def __exit__(self, *exc):
+        import torch
+        if self.old != self.dev.index:
+            torch.cuda.set_device(self.old)
+
+
+def _token_rows(t, name, rows, heads, D):
+    """A [rows, heads, D] bf16 tensor whose rows may be strided (a slice of a
+    fused projection).  Returns the row stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads or 'n_h', D)}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads and columns of a row must be contiguous")
+    return t.stride(0) if rows > 1 else t.shape[1] * D
+
+
+def paged_append(kv: PagedKV, batch: PagedBatch, k, v, cos=None, sin=None, *, q=None, interleaved: bool = False,
+                 q_out=None):
+    """Appends k and v [total_q, n_kv, D] bf16 to the cache at the batch's
+    positions, rotating k (and q [total_q, n_h, D], if given) by the angles
+    cos and sin [n_pos, rot/2] f32 of each position on the way; see
+    dsa_paged_append.  Row strides are free.  Returns the rotated queries
+    (q_out) or None."""
+    import torch
+    d = kv.desc
+    rows = batch.desc.total_q
+    ks, vs = _token_rows(k, "k", rows, d.n_kv, d.D), _token_rows(v, "v", rows, d.n_kv, d.D)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    n_pos = rot = 0
+    if cos is not None:
+        _need(cos, torch.float32, name="cos")
+        _need(sin, torch.float32, cos.shape, "sin")
+        if cos.dim() != 2:
+            raise ValueError("cos must be [n_pos, rot/2]")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    n_h = qs = 0
+    if q is not None:
+        qs, n_h = _token_rows(q, "q", rows, None, d.D), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((rows, n_h, d.D), dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, (rows, n_h, d.D), "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    _same_device(kv.k, batch.cu_q, k, v, cos, sin, q, q_out)
+    with _on(kv.k) as stream:
+        _check(lib().dsa_paged_append(kv.ref, batch.ref, _ptr(k), ks, _ptr(v), vs, _ptr(cos), _ptr(sin), n_pos, rot,
+                                      int(interleaved), _ptr(q), qs, n_h, _ptr(q_out), stream))
+    return q_out
+
+
+def page_topk(q, kv: PagedKV, batch: PagedBatch, n_sel: int, *, n_first: int = 1, n_last: int = 1,
+              inclusive: bool = False, out=None):
+    """Selects n_sel pages per row and key/value head by the cheap score of
+    dsa_page_topk.  q [total_q, n_h, D] bf16 (rotated); returns sel [total_q,
+    n_kv, n_sel] int32 (ascending page numbers, then -1)."""
+    import torch
+    d = kv.desc
+    rows = batch.desc.total_q
+    _need(q, torch.bfloat16, name="q")
+    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d.D:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', d.D)}")
+    if out is None:
+        out = torch.empty((rows, d.n_kv, n_sel), dtype=torch.int32, device=q.device)
+    _need(out, torch.int32, (rows, d.n_kv, n_sel), "out")
+    _same_device(kv.k, batch.cu_q, q, out)
+    with _on(q) as stream:
+        _check(lib().dsa_page_topk(_ptr(q), q.shape[1], kv.ref, batch.ref, int(inclusive), n_sel, n_first, n_last,
+                                   _ptr(out), stream))
+    return out
+
+
+def paged_attn_workspace(kv: PagedKV, batch: PagedBatch, n_h: int, n_sel: int = 0) -> int:
+    return int(lib().dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel))
+
+
+def paged_attn(q, kv: PagedKV, batch: PagedBatch, scale: float, *, sel=None, inclusive: bool = False, out=None,
+               lse=None, ws=None):
+    """Attention of q [total_q, n_h, D] bf16 over the cache: every visible
+    position, or those in the pages of sel [total_q, n_kv, n_sel] int32.
+    Returns out [total_q, n_h, D] bf16 (and fills lse [total_q, n_h] f32 if
+    given); see dsa_paged_attn."""
+    import torch
+    d = kv.desc
+    rows = batch.desc.total_q
+    _need(q, torch.bfloat16, name="q")
+    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d.D:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', d.D)}")
+    n_h, n_sel = q.shape[1], 0
+    if sel is not None:
+        n_sel = sel.shape[-1]
+        _need(sel, torch.int32, (rows, d.n_kv, n_sel), "sel")
+    if out is None:
+        out = torch.empty((rows, n_h, d.D), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, (rows, n_h, d.D), "out")
+    if lse is not None:
+        _need(lse, torch.float32, (rows, n_h), "lse")
+    _same_device(kv.k, batch.cu_q, q, sel, out, lse, ws)
+    with _on(q) as stream:
+        if ws is None:
+            ws = torch.empty(max(paged_attn_workspace(kv, batch, n_h, n_sel), 16), dtype=torch.uint8, device=q.device)
+        _check(lib().dsa_paged_attn(_ptr(q), n_h, kv.ref, batch.ref, int(inclusive), _ptr(sel), n_sel, float(scale),
+                                    _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), stream))
+    return out
+
+
+def check_paged(kv: PagedKV, batch: PagedBatch) -> int:
+    """Number of sequences of the batch that break the dsa_paged_batch
+    contract (checked on the device).  Synchronises the current stream."""
+    import torch
+    bad = torch.empty(1, dtype=torch.int32, device=batch.cu_q.device)
+    with _on(bad) as stream:
+        _check(lib().dsa_check_paged(kv.ref, batch.ref, _ptr(bad), stream))
+    return int(bad.item())
