@@ -335,8 +335,8 @@ typedef struct {
  * before its slot 0 is written is forgotten.
  * Summaries (when kv->sum is given) are written for the pages that this call
  * completes, from the cached (rounded) keys: their sum over the slots by
- * halving (slot i + slot i + page/2, ...) in f32, codes rint(sum * (127 /
- * amax)), scale (amax / 127) / page; a page whose sum is not finite, or
+ * halving (slot i + slot i + page/2, ...) in f32, codes rint(sum * (127 * (1 /
+ * amax))), scale (amax * (1 / 127)) / page, each operation rounded to f32; a page whose sum is not finite, or
  * below 3.8e-37 everywhere, gets zeros. */
 dsa_status dsa_paged_append(const dsa_paged_kv *kv, const dsa_paged_batch *batch,
                             const dsa_bf16 *k, int64_t k_row_stride, const dsa_bf16 *v,
@@ -348,7 +348,7 @@ dsa_status dsa_paged_append(const dsa_paged_kv *kv, const dsa_paged_batch *batch
  * sequence that score best, among the n = ceil(visible positions / page) pages
  * the row sees.  q [total_q, n_h, D] bf16, n_h a multiple of n_kv.  With the
  * head group's pooled query qs = sum of its n_h / n_kv query heads (formed
- * exactly and rounded to f32), c = rint(qs * (127 / amax qs)):
+ * exactly and rounded to f32), c = rint(qs * (127 * (1 / amax qs))):
  *   score(p) = f32(sum_d c[d] * sum[p, d]) * sum_scale[p].
  * The dot is a whole number below 2^24, so the score is the same however it
  * is computed.  The first n_first and the last n_last pages that the row sees

@@ -70,7 +70,7 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 constexpr float kMaxF32 = 3.402823466e38f;
-constexpr float kMinTop = 3.8e-37f;  // 127 / amax stays finite above it
+constexpr float kMinTop = 3.8e-37f;  // 127 * (1 / amax) stays finite above it
 
 // Eight consecutive columns (from column c) of a head's row x, rotated by the
 // angles of position pos.  Products and sums are rounded one by one (no fused
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   top = block_max(top, red);
   fine = fine && top >= kMinTop;
   if (g == 0) {
-    const float inv = __fdiv_rn(127.f, top);
+    const float inv = __fmul_rn(127.f, __frcp_rn(top));
     uint32_t w[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       w[i >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (i & 3));
     }
     *reinterpret_cast<uint2*>(p.a.sum + unit * D + c) = make_uint2(w[0], w[1]);
-    if (vec == 0) p.a.sum_scale[unit] = fine ? __fmul_rn(__fdiv_rn(top, 127.f), 1.f / PAGE) : 0.f;
+    if (vec == 0) p.a.sum_scale[unit] = fine ? __fmul_rn(__fmul_rn(top, 1.f / 127.f), 1.f / PAGE) : 0.f;
   }
 }
 
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   }
   const bool fine = __syncthreads_and(fabsf(qs) <= kMaxF32);
   const float amax = block_max(fabsf(qs), red);
-  if (tid < D) qc[tid] = fine && amax >= kMinTop ? static_cast<int8_t>(__float2int_rn(__fmul_rn(qs, __fdiv_rn(127.f, amax)))) : 0;
+  if (tid < D) qc[tid] = fine && amax >= kMinTop ? static_cast<int8_t>(__float2int_rn(__fmul_rn(qs, __fmul_rn(127.f, __frcp_rn(amax))))) : 0;
   __syncthreads();
   for (int j = tid; j < n; j += kSelThreads) {
     uint32_t key = 0xffffffffu;

@@ -86,7 +86,8 @@ class Cache:
                     for h in range(total.shape[0]):
                         top = float(total[h].abs().max())
                         ok = math.isfinite(top) and top >= 3.8e-37
-                        self.sum[pg, h] = (total[h] * (127.0 / top)).round().to(torch.int8) if ok else 0
+                        inv = torch.tensor(top).float().reciprocal() * 127.0 if ok else 0.0
+                        self.sum[pg, h] = (total[h].float() * inv).round().to(torch.int8) if ok else 0
                         self.sum_scale[pg, h] = top / 127.0 / self.page if ok else 0.0
             at += n
 
@@ -106,7 +107,7 @@ def select_row(q_group, codes, scales, n, n_sel, n_first, n_last):
     qs = q_group.sum(0).float()
     top = qs.abs().max()
     ok = bool(torch.isfinite(top)) and float(top) >= 3.8e-37
-    c = (qs * (torch.tensor(127.0) / top)).round().to(torch.int64) if ok else torch.zeros(qs.shape, dtype=torch.int64)
+    c = (qs * (top.reciprocal() * 127.0)).round().to(torch.int64) if ok else torch.zeros(qs.shape, dtype=torch.int64)
     dots = (codes.to(torch.int64) * c).sum(1).float()
     score = [float(x) for x in dots * scales.float()]
     key = [(-math.inf if (p < n_first or p >= n - n_last) else -score[p], p) for p in range(n)]
