@@ -78,6 +78,18 @@ bool encode_tiled_2d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tiled_4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&stride_bytes)[3], uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t strides[3] = {stride_bytes[0], stride_bytes[1], stride_bytes[2]};
+  const cuuint32_t box[4] = {box0, box1, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, dtype, 4, const_cast<void*>(base), d, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 unsigned int* device_error_word() {
   static unsigned int* cache[64] = {nullptr};
   int dev = 0;

@@ -25,6 +25,9 @@ bool encode_tiled_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d
                      CUtensorMapSwizzle swizzle,
                      CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 
+bool encode_tiled_4d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&stride_bytes)[3], uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
+
 // Raises a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device, calling the runtime only the first time per (device, kernel)
 // and size (launch paths stay cheap when called every layer).

@@ -1,5 +1,16 @@
 // paged_attn.cu -- attention over a paged key/value cache (include/dsa.h,
 // dsa_paged_attn): all pages of a sequence, or the selected ones.
+//
+// paged_attn_kernel puts KEYS on the 128 rows of the tensor-core tile and the
+// few query heads that share them on the columns, so that a decode row wastes
+// no tensor work on padding and the cache streams from HBM straight into the
+// MMA's operands:
+//     S^T[128 keys, N] = K . Q^T        A = K tile (K-major),  B = Q rows
+//     O^T[D, N]       += V^T . P        A = V tile (MN-major), B = P rows
+// An 8-bit cache is never widened.  E4M3 x E4M3 products are exact, and the
+// 16-bit operands are split into two E4M3 terms, x = hi + lo / 32, which hold
+// the 8 significant bits of a bf16 value exactly: the columns are the heads'
+// hi terms, then their lo terms, with an accumulator each (N = 2 heads).
 #include <algorithm>
 #include <string>
 
@@ -8,111 +19,805 @@
 namespace dsa {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = 128;         // keys per tile
+constexpr int kMaxCtas = 320;      // CTAs that may leave partial results
+constexpr int kNoPage = 1 << 30;   // position of a slot that no page holds
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct PattnParams {
   PagedArgs a;
   const dsa_bf16* q;
   const int32_t* sel;
-  int n_h, page, inclusive, n_sel;
-  float scale;
+  int n_h, G, page, shift, ppt, inclusive, n_sel;  // shift: log2 page; ppt: pages per tile
+  int Gx, R, hbs, max_rb;  // heads and rows of a unit, head blocks, row blocks
+  int tpu, aligned;        // sparse: tiles per unit; whole units per CTA
+  float scale_log2;
   dsa_bf16* out;
   float* lse;
+  float* part_o;           // [2 CTAs][NH][D]
+  float* part_l;           // [2 CTAs][NH]
+  int2* meta;              // [units] first and last CTA of a split unit
+  unsigned int* err;
 };
 
-// One block per (row, key/value head); thread = key in the score step and
-// thread = column in the value step.  Running maximum and sum per head.
-template <int D, bool F8>
-__global__ void __launch_bounds__(kTile) paged_attn_simple_kernel(const PattnParams p) {
-  extern __shared__ float sm[];
-  const int G = p.n_h / p.a.n_kv, tid = threadIdx.x;
-  float* qf = sm;                 // [G][D]
-  float* w = qf + G * D;          // [G][kTile]
-  float* o = w + G * kTile;       // [G][D]
-  float* ml = o + G * D;          // [G][3]: max, sum, factor
-  __shared__ int unit_of[kTile], base_of[kTile];
-  const int row = blockIdx.x / p.a.n_kv, head = blockIdx.x % p.a.n_kv;
+// A unit is what one accumulator holds: R consecutive rows of a sequence (one
+// row when pages are selected) x Gx heads of one key/value head.  A segment is
+// a CTA's run of a unit's tiles.
+struct Seg {
+  int b, row0, nr, kvh, h0, nh, t0, t1;  // rows; heads; visible positions of the first and last row
+  int lo, hi;                            // tiles
+  int unit, slot;                        // slot -1: the whole unit, 1: its beginning, 0: a later part
+  int last_cta;
+};
+
+// The tiles of all units in a row, cut into equal runs, one per CTA: equal
+// work whatever the sequences' lengths.  Every role of a CTA walks its run by
+// itself; all lanes of a warp call together.
+template <bool SPARSE>
+struct Walker {
+  const PattnParams& p;
+  long long pos, end, total;
+  long long base, weight;  // dense: first tile and tiles of the current sequence
+  int b, r0, n, nrb, tiles;
+
+  __device__ __forceinline__ long long seq(int s, int& r, int& rows, int& blocks, int& t) const {
+    paged_rows(p.a, s, r, rows);
+    blocks = (rows + p.R - 1) / p.R;
+    t = rows ? max(1, (paged_visible(p.a, s, rows - 1, p.inclusive) + kTile - 1) / kTile) : 1;
+    return static_cast<long long>(blocks) * p.a.n_kv * p.hbs * t;
+  }
+
+  __device__ __forceinline__ explicit Walker(const PattnParams& pp) : p(pp) {
+    const long long c = blockIdx.x, C = gridDim.x;
+    if constexpr (SPARSE) {
+      const long long units = static_cast<long long>(p.a.total_q) * p.a.n_kv * p.hbs;
+      total = units * p.tpu;
+      pos = p.aligned ? units * c / C * p.tpu : total * c / C;
+      end = p.aligned ? units * (c + 1) / C * p.tpu : total * (c + 1) / C;
+    } else {
+      const int lane = threadIdx.x & 31;
+      int r, rows, blocks, t;
+      total = 0;
+      for (int s0 = 0; s0 < p.a.B; s0 += 32) {
+        long long w = s0 + lane < p.a.B ? seq(s0 + lane, r, rows, blocks, t) : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        total += w;
+      }
+      pos = total * c / C;
+      end = total * (c + 1) / C;
+      base = 0;
+      b = 0;
+      for (int s0 = 0; s0 < p.a.B; s0 += 32) {  // the sequence that holds tile pos
+        long long w = s0 + lane < p.a.B ? seq(s0 + lane, r, rows, blocks, t) : 0;
+        const long long own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, w, o);
+          if (lane >= o) w += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, base + w > pos);
+        if (over) {
+          const int f = __ffs(over) - 1;
+          b = s0 + f;
+          base += __shfl_sync(0xffffffffu, w - own, f);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, w, 31);
+      }
+      weight = b < p.a.B ? seq(b, r0, n, nrb, tiles) : 0;
+    }
+  }
+
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (pos >= end) return false;
+    long long u, nominal;
+    if constexpr (SPARSE) {
+      u = pos / p.tpu;
+      s.lo = static_cast<int>(pos - u * p.tpu);
+      nominal = p.tpu;
+      s.unit = static_cast<int>(u);
+      s.row0 = static_cast<int>(u % p.a.total_q);
+      const int rem = static_cast<int>(u / p.a.total_q);
+      s.kvh = rem / p.hbs;
+      s.h0 = rem % p.hbs * p.Gx;
+      s.b = paged_seq(p.a, s.row0);
+      s.nr = 1;
+      s.t0 = s.t1 = paged_visible(p.a, s.b, s.row0 - __ldg(p.a.cu_q + s.b), p.inclusive);
+    } else {
+      while (pos >= base + weight) {
+        base += weight;
+        weight = seq(++b, r0, n, nrb, tiles);
+      }
+      u = (pos - base) / tiles;
+      s.lo = static_cast<int>(pos - base - u * tiles);
+      nominal = tiles;
+      const int rb = static_cast<int>(u % nrb), rem = static_cast<int>(u / nrb);
+      s.kvh = rem / p.hbs;
+      s.h0 = rem % p.hbs * p.Gx;
+      s.b = b;
+      s.unit = ((b * p.a.n_kv + s.kvh) * p.hbs + rem % p.hbs) * p.max_rb + rb;
+      s.row0 = r0 + rb * p.R;
+      s.nr = min(p.R, n - rb * p.R);
+      s.t0 = paged_visible(p.a, b, rb * p.R, p.inclusive);
+      s.t1 = paged_visible(p.a, b, rb * p.R + s.nr - 1, p.inclusive);
+    }
+    s.nh = min(p.Gx, p.G - s.h0) * s.nr;
+    const long long left = end - pos;
+    s.hi = static_cast<int>(min(nominal, s.lo + left));
+    const long long unit_end = pos - s.lo + nominal;
+    pos += s.hi - s.lo;
+    s.slot = s.lo == 0 ? (s.hi == nominal ? -1 : 1) : 0;
+    s.last_cta = static_cast<int>((unit_end * gridDim.x - 1) / total);
+    if constexpr (!SPARSE) {  // earlier rows end earlier than the sequence
+      const int own = max(1, (s.t1 + kTile - 1) / kTile);
+      s.lo = min(s.lo, own);
+      s.hi = min(s.hi, own);
+    }
+    return true;
+  }
+};
+
+template <int D, bool F8, int NH>
+struct Cfg {
+  static constexpr int kHG = NH < 16 ? NH : 16;      // heads per epilogue group of four warps
+  static constexpr int kGroups = NH / kHG;
+  static constexpr int kEpiWarps = 4 * kGroups;
+  static constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+  static constexpr int kThreads = 32 * (kEpiWarps + 2);
+  static constexpr int kCtasPerSm = NH <= 16 ? 2 : 1;
+  static constexpr int kElem = F8 ? 1 : 2;
+  static constexpr int kN = F8 ? 2 * NH : (NH < 16 ? 16 : NH);  // MMA columns
+  static constexpr int kRow = D * kElem;                        // bytes of a cached row
+  static constexpr int kRowB = kRow < 128 ? kRow : 128;         // bytes of a row in a tile slab
+  static constexpr int kSlabs = kRow / kRowB;
+  static constexpr uint32_t kSwz = kRowB == 128 ? kSwizzle128B : kSwizzle64B;
+  static constexpr int kSlabBytes = kTile * kRowB;
+  static constexpr int kEntry = kTile * kRow;                   // a K or V tile
+  static constexpr int kQBytes = kN * kRow;
+  static constexpr int kPBytes = kN * kTile * kElem;
+  static constexpr int kRing = (NH <= 16 ? 96 : 176) * 1024 / kEntry;  // entries: K, V, K, V, ...
+  static constexpr int kMetas = kRing / 2 + 3;  // a slot is rewritten only after the PV of its tile
+  static constexpr int kMetaBytes = kMetas * 8 * 16;
+  static constexpr int kWm = kGroups * 2 * 4 * (kHG + 4);
+  static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
+  static constexpr int kSmem = 1024 + kRing * kEntry + kQBytes + 2 * kPBytes + kMetaBytes + kWm * 4 + 2 * NH * 4 +
+                               4 * NH * 4 + 8 * (2 * kRing + kMetas + 8) + 64;
+  static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+// Byte offset of row n, byte column c of a K-major operand slab with rows of
+// ROWB bytes (swizzled in 16-byte chunks).
+template <int ROWB>
+__device__ __forceinline__ uint32_t op_off(int n, int c) {
+  const int sw = ROWB == 128 ? (n & 7) : ((n >> 1) & 3);
+  return n * ROWB + ((((c >> 4) ^ sw) << 4) | (c & 15));
+}
+
+// Warps 0 .. 4 groups - 1: softmax and output (thread = key in the scores,
+// = column of D in the output); then one TMA warp and one MMA warp.  Bound by
+// the cache's bytes for decode: the ring keeps 96 KB per CTA in flight.
+template <int D, bool F8, int NH, bool SPARSE>
+__global__ void __launch_bounds__(Cfg<D, F8, NH>::kThreads, Cfg<D, F8, NH>::kCtasPerSm)
+paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const PattnParams p) {
+  using C = Cfg<D, F8, NH>;
+  constexpr int HG = C::kHG, kRing = C::kRing, kMetas = C::kMetas;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem;
+  uint8_t* q_smem = ring + kRing * C::kEntry;
+  uint8_t* p_smem = q_smem + C::kQBytes;
+  int4* meta = reinterpret_cast<int4*>(p_smem + 2 * C::kPBytes);  // [kMetas][8] position, K scale, V scale
+  float* wm = reinterpret_cast<float*>(meta + kMetas * 8);        // [group][2][4 warps][HG + 4]
+  float* cq = wm + C::kWm;                                        // [2][NH] factor of a head's scores
+  float* lsum = cq + 2 * NH;                                      // [4 warps][NH]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(lsum + 4 * NH);
+  uint64_t *full = bars, *empty = full + kRing, *meta_full = empty + kRing;
+  uint64_t *s_full = meta_full + kMetas, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* poison = abort_flag + 1;  // [2] a value that not every row of the unit sees is not finite
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], C::kEpiWarps); mbar_init(&pv_done[i], 1); }
+    mbar_init(q_full, C::kEpiWarps);
+    *abort_flag = 0;
+    poison[0] = poison[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if constexpr (C::kN > NH && !F8)  // the padding rows of Q and P stay zero
+    for (int i = threadIdx.x; i < (C::kQBytes + 2 * C::kPBytes) / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(q_smem)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_o = tmem + 2 * C::kN;
   pdl_trigger();
   pdl_wait();
-  const int b = paged_seq(p.a, row);
-  const int t = paged_visible(p.a, b, row - __ldg(p.a.cu_q + b), p.inclusive);
-  const int pages = (t + p.page - 1) / p.page;
-  for (int e = tid; e < G * D; e += kTile) {
-    qf[e] = __uint_as_float(static_cast<uint32_t>(p.q[(static_cast<int64_t>(row) * p.n_h + head * G) * D + e]) << 16) * p.scale;
-    o[e] = 0.f;
-  }
-  for (int h = tid; h < G; h += kTile) { ml[3 * h] = -INFINITY; ml[3 * h + 1] = 0.f; }
-  const int n_list = p.sel ? p.n_sel : pages;
-  const int per = kTile / p.page;
-  for (int l0 = 0; l0 < n_list; l0 += per) {
-    __syncthreads();
-    const int l = l0 + tid / p.page;
-    int j = -1;
-    if (l < n_list) j = p.sel ? __ldg(p.sel + (static_cast<int64_t>(row) * p.a.n_kv + head) * p.n_sel + l) : l;
-    const int pg = j >= 0 && j < pages ? paged_page(p.a, b, j) : -1;
-    const bool seen = pg >= 0 && j * p.page + tid % p.page < t;
-    const int64_t unit = seen ? static_cast<int64_t>(pg) * p.a.n_kv + head : 0;
-    unit_of[tid] = seen ? static_cast<int>(unit) : -1;
-    const int64_t at = (unit * p.page + tid % p.page) * D;
-    for (int h = 0; h < G; ++h) {
-      float acc = 0.f;
-      if (seen) {
-        for (int c = 0; c < D; ++c) {
-          float x;
-          if constexpr (F8) x = e4m3x2_to_f32(static_cast<const uint8_t*>(p.a.k)[at + c]).x;
-          else x = __uint_as_float(static_cast<uint32_t>(static_cast<const dsa_bf16*>(p.a.k)[at + c]) << 16);
-          acc = fmaf(x, qf[h * D + c], acc);
+
+  Walker<SPARSE> walk(p);
+  Seg s;
+  if (warp == C::kTmaWarp) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) { tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
+    const int per = 32 / p.ppt;  // tiles whose pages one load of the warp covers
+    int it = 0;
+    bool ok = true;
+    while (ok && walk.next(s)) {
+      const int n_list = SPARSE ? p.n_sel : (s.t1 + p.page - 1) / p.page;
+      const int n_vis = (s.t1 + p.page - 1) / p.page;
+      const int32_t* list = SPARSE ? p.sel + (static_cast<int64_t>(s.row0) * p.a.n_kv + s.kvh) * p.n_sel : nullptr;
+      const auto fetch = [&](int tile0, int& j, int& pg, float& ks, float& vs) {
+        const int l = tile0 * p.ppt + lane;
+        j = -1;
+        if (l < n_list) j = SPARSE ? __ldg(list + l) : l;
+        pg = j >= 0 && j < n_vis ? paged_page(p.a, s.b, j) : -1;
+        ks = vs = 0.f;
+        if (F8 && pg >= 0) {
+          const int64_t u = static_cast<int64_t>(pg) * p.a.n_kv + s.kvh;
+          ks = __ldg(p.a.k_scale + u);
+          vs = __ldg(p.a.v_scale + u);
         }
-        if constexpr (F8) acc *= p.a.k_scale[unit];
+      };
+      int j, pg, jn, pn;
+      float ks, vs, kn, vn;
+      fetch(s.lo, jn, pn, kn, vn);
+      for (int i = s.lo; i < s.hi; ++i, ++it) {
+        const int in = (i - s.lo) % per;
+        if (in == 0) {
+          j = jn; pg = pn; ks = kn; vs = vn;
+          if (i + per < s.hi) fetch(i + per, jn, pn, kn, vn);
+        }
+        const int src = in * p.ppt + lane % p.ppt;
+        const int mj = __shfl_sync(0xffffffffu, j, src), mp = __shfl_sync(0xffffffffu, pg, src);
+        const float mk = __shfl_sync(0xffffffffu, ks, src), mv = __shfl_sync(0xffffffffu, vs, src);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int e = 2 * it + kv, st = e % kRing;
+          ok = ok && mbar_wait(&empty[st], ((e / kRing) & 1) ^ 1, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (kv == 0) {
+            if (lane < p.ppt)
+              meta[it % kMetas * 8 + lane] = make_int4(mp >= 0 ? mj * p.page : kNoPage, __float_as_int(mk), __float_as_int(mv), 0);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&meta_full[it % kMetas]);
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kEntry);
+          __syncwarp();
+          // a slot without a page reads outside the pool: zeros
+          if (lane < p.ppt)
+#pragma unroll
+            for (int c = 0; c < C::kSlabs; ++c)
+              tma_load_4d(ring + st * C::kEntry + c * C::kSlabBytes + lane * p.page * C::kRowB, kv ? &tm_v : &tm_k, &full[st],
+                          c * (128 / C::kElem), 0, s.kvh, mp >= 0 ? mp : p.a.n_pages);
+        }
+        if (!ok) break;
       }
-      w[h * kTile + tid] = seen ? acc : -INFINITY;
     }
-    __syncthreads();
-    for (int h = tid >> 5; h < G; h += kTile / 32) {
-      const int lane = tid & 31;
-      float m = -INFINITY;
-      for (int e = lane; e < kTile; e += 32) m = fmaxf(m, w[h * kTile + e]);
-      for (int s = 16; s; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-      const float mo = ml[3 * h], mn = fmaxf(mo, m), mu = mn == -INFINITY ? 0.f : mn;
-      float sum = 0.f;
-      for (int e = lane; e < kTile; e += 32) {
-        const float x = expf(w[h * kTile + e] - mu);
-        w[h * kTile + e] = x;
-        sum += x;
+    if (!ok && lane == 0) {  // let the loads in flight land
+      for (int st = 0; st < kRing; ++st)
+        for (int w = 0; w < 64 && 2 * it > st; ++w)
+          if (mbar_try_wait(smem_u32(&full[st]), ((2 * it - 1 - st) / kRing) & 1)) break;
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---------------------------------------------------------------- MMA
+    constexpr uint32_t idesc_qk = F8 ? make_idesc_f8(128, C::kN, 0, 0) : make_idesc_bf16(128, C::kN, 0, 0);
+    constexpr uint32_t idesc_pv = F8 ? make_idesc_f8(128, C::kN, 1, 0) : make_idesc_bf16(128, C::kN, 1, 0);
+    const uint32_t q_base = smem_u32(q_smem);
+    int it = 0, seg = 0;
+    bool ok = true;
+    const auto qk = [&](int t) {  // S(t) = K(t) Q^T
+      const int e = 2 * t, st = e % kRing;
+      if (!mbar_wait(&full[st], (e / kRing) & 1, abort_flag)) return false;
+      tc_fence_after();
+      const uint32_t kb = smem_u32(ring + st * C::kEntry);
+#pragma unroll
+      for (int k = 0; k < C::kRow / 32; ++k) {
+        constexpr int kPer = C::kRowB / 32;
+        const uint64_t ad = make_smem_desc(kb + k / kPer * C::kSlabBytes + k % kPer * 32, 16, 8 * C::kRowB, C::kSwz);
+        const uint64_t bd = make_smem_desc(q_base + k / kPer * (C::kN * C::kRowB) + k % kPer * 32, 16, 8 * C::kRowB, C::kSwz);
+        if constexpr (F8) umma_f8_ss(tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
+        else umma_bf16_ss(tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
       }
-      for (int s = 16; s; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      __syncwarp();
+      umma_commit(&empty[st]);
+      umma_commit(&s_full[t & 1]);
+      return true;
+    };
+    while (ok && walk.next(s)) {
+      const int n = s.hi - s.lo;
       if (lane == 0) {
-        const float f = expf(mo - mu);
-        ml[3 * h] = mn;
-        ml[3 * h + 1] = ml[3 * h + 1] * f + sum;
-        ml[3 * h + 2] = f;
-      }
-    }
-    __syncthreads();
-    if (tid < D)
-      for (int h = 0; h < G; ++h) {
-        float acc = o[h * D + tid] * ml[3 * h + 2];
-        for (int e = 0; e < kTile; ++e) {
-          if (unit_of[e] < 0) continue;
-          const int64_t va = (static_cast<int64_t>(unit_of[e]) * p.page + e % p.page) * D + tid;
-          float x;
-          if constexpr (F8) x = e4m3x2_to_f32(static_cast<const uint8_t*>(p.a.v)[va]).x * p.a.v_scale[unit_of[e]];
-          else x = __uint_as_float(static_cast<uint32_t>(static_cast<const dsa_bf16*>(p.a.v)[va]) << 16);
-          acc = fmaf(w[h * kTile + e], x, acc);
+        ok = mbar_wait(q_full, seg & 1, abort_flag) && (n == 0 || qk(it));
+        for (int i = 0; ok && i < n; ++i) {
+          const int t = it + i;
+          if (i + 1 < n && !qk(t + 1)) { ok = false; break; }
+          const int e = 2 * t + 1, st = e % kRing;
+          ok = mbar_wait(&p_full[t & 1], (t >> 1) & 1, abort_flag) && mbar_wait(&full[st], (e / kRing) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t vb = smem_u32(ring + st * C::kEntry), pb = smem_u32(p_smem + (t & 1) * C::kPBytes);
+          // V is MN-major: D on the rows.  D = 64 fills only half of the 128
+          // rows; the second half repeats it (stride 0) and is not read.
+          constexpr int kKeys = 32 / C::kElem;  // keys per MMA
+#pragma unroll
+          for (int k = 0; k < kTile / kKeys; ++k) {
+            const uint64_t ad = make_smem_desc(vb + k * kKeys * C::kRowB, D == 128 ? C::kSlabBytes : 0, 8 * C::kRowB, C::kSwz);
+            const uint64_t bd = make_smem_desc(pb + k / 4 * (C::kN * 128) + k % 4 * 32, 16, 1024, kSwizzle128B);
+            if constexpr (F8) umma_f8_ss(tmem_o, ad, bd, idesc_pv, (i | k) != 0);
+            else umma_bf16_ss(tmem_o, ad, bd, idesc_pv, (i | k) != 0);
+          }
+          umma_commit(&empty[st]);
+          umma_commit(&pv_done[t & 1]);
         }
-        o[h * D + tid] = acc;
       }
-  }
-  __syncthreads();
-  if (tid < D)
-    for (int h = 0; h < G; ++h) {
-      const float l = ml[3 * h + 1];
-      const int64_t r = static_cast<int64_t>(row) * p.n_h + head * G + h;
-      const __nv_bfloat16 x = __float2bfloat16_rn(l == 0.f ? 0.f : o[h * D + tid] / l);
-      p.out[r * D + tid] = *reinterpret_cast<const dsa_bf16*>(&x);
-      if (p.lse && tid == 0) p.lse[r] = l == 0.f ? -INFINITY : ml[3 * h] + logf(l);
+      ok = __all_sync(0xffffffffu, ok);
+      it += n;
+      ++seg;
     }
+  } else {
+    // ---------------------------------------------------------------- softmax and output
+    const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const int gh = grp * HG;  // first head of the group
+    float* wmg = wm + grp * 2 * 4 * (HG + 4);
+    int it = 0, seg = 0;
+    bool ok = true;
+
+    // Q rows of a segment as the MMA's B operand (8 columns per thread)
+    const auto load_q = [&](const Seg& g, int par) {
+      constexpr int kVecs = D / 8, kStep = C::kEpiWarps * 32 / kVecs;
+      const int vec = threadIdx.x % kVecs;
+      const int heads = min(p.Gx, p.G - g.h0);
+#pragma unroll
+      for (int n0 = 0; n0 < NH; n0 += kStep) {
+        const int n = n0 + threadIdx.x / kVecs;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (n < g.nh) {
+          const int r = n / heads;
+          w = __ldg(reinterpret_cast<const uint4*>(
+              p.q + (static_cast<int64_t>(g.row0 + r) * p.n_h + g.kvh * p.G + g.h0 + (n - r * heads)) * D + vec * 8));
+        }
+        if constexpr (F8) {
+          float f[8], amax = 0.f;
+          bf16x8_to_f32(w, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (!(fabsf(f[i]) <= 3.4e38f)) f[i] = __int_as_float(0x7fffffff);  // the scores become NaN
+            amax = fmaxf(amax, fabsf(f[i]));
+          }
+#pragma unroll
+          for (int o = kVecs / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // X = the power of two with amax <= 256 X: hi rounds off at most 8
+          const uint32_t u = __float_as_uint(amax);
+          const int ex = max(static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) ? 1 : 0), -100);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = f[2 * i] * inv, b = f[2 * i + 1] * inv;
+            hi[i] = e4m3x2(a, b);
+            const float2 h = e4m3x2_to_f32(hi[i]);
+            lo[i] = e4m3x2((a - h.x) * 32.f, (b - h.y) * 32.f);
+          }
+          if (n < NH) {
+            *reinterpret_cast<uint2*>(q_smem + op_off<C::kRowB>(n, vec * 8)) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(q_smem + op_off<C::kRowB>(NH + n, vec * 8)) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            if (vec == 0) cq[par * NH + n] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) * p.scale_log2;
+          }
+        } else {
+          if (n < NH) *reinterpret_cast<uint4*>(q_smem + vec / 8 * (C::kN * 128) + op_off<128>(n, vec % 8 * 16)) = w;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+
+    bool more = walk.next(s);
+    if (more) load_q(s, 0);
+    else if (p.part_l && threadIdx.x < NH) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;  // no part of any unit
+    while (ok && more) {
+      float m[HG], mp[HG], l[HG];  // reference exponents of the weights and of the weighted V scales; sums
+#pragma unroll
+      for (int h = 0; h < HG; ++h) { m[h] = -INFINITY; mp[h] = -INFINITY; l[h] = 0.f; }
+      const int heads = min(p.Gx, p.G - s.h0);
+      if (F8) ok = mbar_wait(q_full, seg & 1, abort_flag);  // the head factors of this segment are written
+      for (int i = s.lo; i < s.hi; ++i, ++it) {
+        const int buf = it & 1;
+        ok = mbar_wait(&meta_full[it % kMetas], (it / kMetas) & 1, abort_flag) && ok;
+        const int4 mt = ok ? meta[it % kMetas * 8 + (key >> p.shift)] : make_int4(kNoPage, 0, 0, 0);
+        const float ks = __int_as_float(mt.y), vs = __int_as_float(mt.z);
+        const int pos = mt.x + (key & (p.page - 1)), past = pos - s.t0;
+        // head row n sees this key from n = nmin on (rows see one position more each)
+        const int nmin = past < 0 ? 0 : (past < s.nr ? (past + 1) * heads : kNoPage);
+        float x[HG];
+        float lvs = 0.f;
+        if constexpr (F8) lvs = __log2f(warp_max_f32(vs));
+        ok = ok && mbar_wait(&s_full[buf], (it >> 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const uint32_t ts = tmem + buf * C::kN + lanes;
+        if constexpr (F8) {
+          uint32_t a[HG], b[HG];
+          tmem_ld32<HG>(ts + gh, a);
+          tmem_ld32<HG>(ts + NH + gh, b);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float v = fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) * (ks * cq[(seg & 1) * NH + gh + h]);
+            x[h] = gh + h >= nmin ? v : -INFINITY;
+          }
+        } else {
+          uint32_t a[HG];
+          tmem_ld32<HG>(ts + gh, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < HG; ++h) x[h] = gh + h >= nmin ? __uint_as_float(a[h]) * p.scale_log2 : -INFINITY;
+        }
+        // ---- the tile's maximum per head, over the four warps
+        {
+          float* w = wmg + (buf * 4 + wq) * (HG + 4);
+          float v = F8 ? lvs : 0.f;
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const float r = warp_max_f32(x[h]);
+            if (lane == h) v = r;
+          }
+          if (lane <= HG) w[lane] = v;
+        }
+        if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
+        bool grew = false;
+        float fo[HG];
+        {
+          const float* w = wmg + buf * 4 * (HG + 4);
+#pragma unroll
+          for (int h0 = 0; h0 < HG; h0 += 4) {
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, tp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 y = *reinterpret_cast<const float4*>(w + q * (HG + 4) + h0);
+              const float yy[4] = {y.x, y.y, y.z, y.w};
+              const float lv = F8 ? w[q * (HG + 4) + HG] : 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                t[e] = fmaxf(t[e], yy[e]);
+                if (F8) tp[e] = fmaxf(tp[e], yy[e] + lv);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int h = h0 + e;
+              const float mn = fmaxf(m[h], ceilf(t[e]));
+              if (mn > m[h]) {
+                const float f = ex2_approx(m[h] - mn);
+                l[h] *= f;
+                fo[h] = f;
+                m[h] = mn;
+                if (!F8) grew = true;
+              } else {
+                fo[h] = 1.f;
+              }
+              if constexpr (F8) {
+                const float pn = fmaxf(mp[h], ceilf(tp[e]));
+                fo[h] = 1.f;
+                if (pn > mp[h]) {
+                  fo[h] = ex2_approx(mp[h] - pn);
+                  mp[h] = pn;
+                  grew = true;
+                }
+              }
+            }
+          }
+        }
+        // ---- weights, as the MMA's B operand.  P(it - 2) has been read.
+        if (it >= 2) ok = mbar_wait(&pv_done[buf], ((it - 2) >> 1) & 1, abort_flag) && ok;
+        uint8_t* pb = p_smem + buf * C::kPBytes;
+        if constexpr (F8) {
+#pragma unroll
+          for (int h = 0; h < HG; h += 2) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mu = m[h + e] == -INFINITY ? 0.f : m[h + e], mpu = mp[h + e] == -INFINITY ? 0.f : mp[h + e];
+              const float pw = ex2_approx(x[h + e] - mu);
+              l[h + e] += pw;
+              w[e] = pw * (vs * ex2_approx(fminf(mu - mpu + 8.f, 120.f)));
+            }
+            const uint32_t hi = e4m3x2(w[0], w[1]);
+            const float2 back = e4m3x2_to_f32(hi);
+            const uint32_t lo = e4m3x2((w[0] - back.x) * 32.f, (w[1] - back.y) * 32.f);
+            pb[op_off<128>(gh + h, key)] = static_cast<uint8_t>(hi);
+            pb[op_off<128>(gh + h + 1, key)] = static_cast<uint8_t>(hi >> 8);
+            pb[op_off<128>(NH + gh + h, key)] = static_cast<uint8_t>(lo);
+            pb[op_off<128>(NH + gh + h + 1, key)] = static_cast<uint8_t>(lo >> 8);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < HG; h += 2) {
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mu = m[h + e] == -INFINITY ? 0.f : m[h + e];
+              w[e] = ex2_approx(x[h + e] - mu);
+              l[h + e] += w[e];
+            }
+            const uint32_t two = pack_bf16(w[0], w[1]);
+            uint8_t* dst = pb + (key >> 6) * (C::kN * 128);
+            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h, (key & 63) * 2)) = static_cast<uint16_t>(two);
+            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(two >> 16);
+          }
+        }
+        // ---- O follows a new reference exponent
+        if (grew && i > s.lo) {  // the same for the whole group
+          ok = mbar_wait(&pv_done[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          if (wq * 32 < D) {
+            constexpr int kParts = F8 && HG == 16 ? 2 : 1;
+#pragma unroll
+            for (int c = 0; c < kParts; ++c) {
+              uint32_t o[16];
+              const uint32_t to = tmem_o + lanes + gh + c * NH;
+              tmem_ld32<16>(to, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 16; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * fo[h % HG]);
+              tmem_st32x16(to, o);
+              tmem_st_wait();
+            }
+          }
+        }
+        // ---- slots that no row of the unit sees hold anything: V = 0 there.
+        // A slot that only later rows see must not reach the earlier ones
+        // through 0 * inf: such values are set aside and added at the end.
+        if (grp == 0 && __any_sync(0xffffffffu, past >= 0 && mt.x != kNoPage)) {
+          const int e = 2 * it + 1, st = e % kRing;
+          ok = mbar_wait(&full[st], (e / kRing) & 1, abort_flag) && ok;
+          if (ok && past >= 0 && mt.x != kNoPage) {
+#pragma unroll
+            for (int c = 0; c < C::kSlabs; ++c) {
+              uint4* row = reinterpret_cast<uint4*>(ring + st * C::kEntry + c * C::kSlabBytes + key * C::kRowB);
+              for (int v = 0; v < C::kRowB / 16; ++v) {
+                uint4 w = row[v];
+                uint32_t y[4] = {w.x, w.y, w.z, w.w};
+                bool bad = pos >= s.t1;
+                if (!bad) {
+#pragma unroll
+                  for (int u = 0; u < 4; ++u) {
+                    const uint32_t gone = F8 ? __vcmpeq4(y[u] & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(y[u] & 0x7f807f80u, 0x7f807f80u);
+                    y[u] &= ~gone;
+                    bad = bad || gone != 0;
+                  }
+                  if (bad) poison[seg & 1] = 1;
+                  if (bad) row[v] = make_uint4(y[0], y[1], y[2], y[3]);
+                } else {
+                  row[v] = make_uint4(0, 0, 0, 0);
+                }
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      // ---- the next segment's queries: every QK of this one is complete
+      Seg cur = s;
+      const int last = it - 1;
+      more = ok && walk.next(s);
+      if (more) load_q(s, (seg + 1) & 1);
+
+      // ---- output of the segment
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (lane == h) lsum[wq * NH + gh + h] = l[h];
+      }
+      const bool any = cur.hi > cur.lo;
+      if (any && ok) ok = mbar_wait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
+      // the other flag's readers (the segment before) are done: every warp has
+      // delivered weights of this segment, and none begins the next one before
+      // the barrier below
+      if (any && threadIdx.x == 0) poison[(seg & 1) ^ 1] = 0;
+      if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
+      tc_fence_after();
+      float o[HG];
+      if constexpr (F8) {
+        uint32_t a[HG], b[HG];
+        tmem_ld32<HG>(tmem_o + lanes + gh, a);
+        tmem_ld32<HG>(tmem_o + lanes + NH + gh, b);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < HG; ++h) o[h] = any ? fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) : 0.f;
+      } else {
+        uint32_t a[HG];
+        tmem_ld32<HG>(tmem_o + lanes + gh, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < HG; ++h) o[h] = any ? __uint_as_float(a[h]) : 0.f;
+      }
+      tc_fence_before();
+#pragma unroll
+      for (int h = 0; h < HG; ++h) {
+        const float* t = lsum + gh + h;
+        l[h] = (t[0] + t[NH]) + (t[2 * NH] + t[3 * NH]);
+        const float f = F8 ? ex2_approx((mp[h] == -INFINITY ? 0.f : mp[h]) - (m[h] == -INFINITY ? 0.f : m[h]) - 8.f) : 1.f;
+        o[h] = l[h] == 0.f ? 0.f : o[h] * f / l[h];
+      }
+      if (poison[seg & 1] && key < D) {  // values that are not finite, for the rows that see them
+        for (int t = max(cur.t0, cur.lo * kTile); t < min(cur.t1, cur.hi * kTile); ++t) {
+          const int pg = paged_page(p.a, cur.b, t / p.page);
+          if (pg < 0) continue;
+          const int64_t at = ((static_cast<int64_t>(pg) * p.a.n_kv + cur.kvh) * p.page + t % p.page) * D + key;
+          float v;
+          if constexpr (F8) v = e4m3x2_to_f32(static_cast<const uint8_t*>(p.a.v)[at]).x;
+          else v = __uint_as_float(static_cast<uint32_t>(static_cast<const dsa_bf16*>(p.a.v)[at]) << 16);
+          if (fabsf(v) <= 3.4e38f) continue;
+#pragma unroll
+          for (int h = 0; h < HG; ++h)
+            if ((gh + h) / heads > t - cur.t0) o[h] += v;
+        }
+      }
+      if (cur.slot < 0) {
+        if (key < D) {
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            const int n = gh + h;
+            if (n < cur.nh) {
+              const int r = n / heads;
+              const int64_t at = static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads);
+              const __nv_bfloat16 y = __float2bfloat16_rn(o[h]);
+              p.out[at * D + key] = *reinterpret_cast<const dsa_bf16*>(&y);
+              if (key == 0 && p.lse) p.lse[at] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
+            }
+          }
+        }
+      } else {
+        const int64_t slot = 2 * blockIdx.x + cur.slot;
+        if (key < D) {
+#pragma unroll
+          for (int h = 0; h < HG; ++h) {
+            p.part_o[(slot * NH + gh + h) * D + key] = o[h];
+            if (key == 0) p.part_l[slot * NH + gh + h] = l[h] == 0.f ? -INFINITY : m[h] + log2f(l[h]);
+          }
+        }
+      }
+      if (threadIdx.x == 0 && cur.slot != 0 && p.meta) p.meta[cur.unit] = cur.slot < 0 ? make_int2(-1, -1) : make_int2(blockIdx.x, cur.last_cta);
+      ++seg;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, 1u);
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the parts of a unit that several CTAs worked on: each part is its
+// normalised output and log2 of its sum.  One block per (unit, head).
+template <int D>
+__global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p, int NH, int sparse) {
+  pdl_trigger();
+  pdl_wait();
+  const int unit = blockIdx.x, n = blockIdx.y, d = threadIdx.x;
+  int row0, nr, kvh, h0;
+  if (sparse) {
+    row0 = unit % p.a.total_q;
+    nr = 1;
+    const int rem = unit / p.a.total_q;
+    kvh = rem / p.hbs;
+    h0 = rem % p.hbs * p.Gx;
+  } else {
+    const int rb = unit % p.max_rb;
+    int rem = unit / p.max_rb;
+    h0 = rem % p.hbs * p.Gx;
+    rem /= p.hbs;
+    kvh = rem % p.a.n_kv;
+    int r0, rows;
+    paged_rows(p.a, rem / p.a.n_kv, r0, rows);
+    row0 = r0 + rb * p.R;
+    nr = min(p.R, rows - rb * p.R);
+  }
+  const int heads = min(p.Gx, p.G - h0);
+  if (nr <= 0 || n >= heads * nr) return;
+  const int2 c = p.meta[unit];
+  if (c.x < 0) return;
+  const auto slot = [&](int i) { return static_cast<int64_t>(2 * i + (i == c.x)) * NH + n; };
+  float top = -INFINITY;
+  for (int i = c.x; i <= c.y; ++i) top = fmaxf(top, p.part_l[slot(i)]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float acc = 0.f, sum = 0.f;
+  for (int i = c.x; i <= c.y; ++i) {
+    const float l2 = p.part_l[slot(i)];
+    const float w = exp2f(l2 - ref);
+    sum += w;
+    if (l2 != -INFINITY) acc += w * p.part_o[slot(i) * D + d];
+  }
+  const int r = n / heads;
+  const int64_t at = static_cast<int64_t>(row0 + r) * p.n_h + kvh * p.G + h0 + (n - r * heads);
+  const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+  p.out[at * D + d] = *reinterpret_cast<const dsa_bf16*>(&y);
+  if (d == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+}
+
+// How a call is cut into units, and what it needs.
+struct Plan {
+  int NH, G, Gx, R, hbs, max_rb, tpu, aligned, grid, merge;
+  long long units;
+  size_t o_bytes, l_bytes, meta_bytes;
+  size_t total() const { return o_bytes + l_bytes + meta_bytes; }
+};
+
+Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n_sel) {
+  Plan pl{};
+  const int G = n_h / kv->n_kv;
+  pl.G = G;
+  // columns of a unit: the group's heads, times a few rows when all pages are read
+  const long long want = n_sel ? G : static_cast<long long>(G) * pb->max_Lq;
+  pl.NH = want <= 8 ? 8 : (want <= 16 ? 16 : 32);
+  pl.Gx = std::min(G, pl.NH);
+  pl.hbs = (G + pl.Gx - 1) / pl.Gx;
+  pl.R = n_sel || pl.hbs > 1 ? 1 : pl.NH / pl.Gx;
+  pl.max_rb = n_sel ? 1 : (pb->max_Lq + pl.R - 1) / pl.R;
+  pl.tpu = n_sel ? (n_sel * kv->page + kTile - 1) / kTile : (pb->max_Lk + kTile - 1) / kTile;
+  pl.units = (n_sel ? static_cast<long long>(pb->total_q) : static_cast<long long>(pb->B) * pl.max_rb) * kv->n_kv * pl.hbs;
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 148;
+  const int ctas = std::min(kMaxCtas, sms * (pl.NH <= 16 ? 2 : 1));
+  pl.aligned = n_sel && pl.units >= 8ll * ctas;
+  pl.grid = static_cast<int>(std::min<long long>(ctas, pl.aligned ? pl.units : std::max(1ll, pl.units * pl.tpu / 2)));
+  pl.merge = !pl.aligned && pl.grid > 1;
+  if (pl.merge) {
+    pl.o_bytes = static_cast<size_t>(2 * kMaxCtas) * pl.NH * kv->D * 4;
+    pl.l_bytes = static_cast<size_t>(2 * kMaxCtas) * pl.NH * 4;
+    pl.meta_bytes = static_cast<size_t>((pl.units + 1) / 2) * 16;
+  }
+  return pl;
+}
+
+template <int D, bool F8, int NH, bool SPARSE>
+cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnParams& p, const Plan& pl, cudaStream_t s) {
+  using C = Cfg<D, F8, NH>;
+  auto fn = paged_attn_kernel<D, F8, NH, SPARSE>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), C::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(fn, dim3(pl.grid), dim3(C::kThreads), C::kSmem, s, k, v, p);
+  if (e == cudaSuccess && pl.merge)
+    e = launch_pdl(paged_attn_merge_kernel<D>, dim3(static_cast<unsigned>(pl.units), NH), dim3(D), 0, s, p, NH, SPARSE ? 1 : 0);
+  return e;
+}
+template <int D, bool F8, int NH>
+cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnParams& p, const Plan& pl, cudaStream_t s) {
+  return p.sel ? launch_attn<D, F8, NH, true>(k, v, p, pl, s) : launch_attn<D, F8, NH, false>(k, v, p, pl, s);
+}
+template <int D, bool F8>
+cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnParams& p, const Plan& pl, cudaStream_t s) {
+  return pl.NH == 8 ? launch_attn<D, F8, 8>(k, v, p, pl, s)
+                    : (pl.NH == 16 ? launch_attn<D, F8, 16>(k, v, p, pl, s) : launch_attn<D, F8, 32>(k, v, p, pl, s));
+}
+
+// Tensor map of a pool: {columns, slots, heads, pages}, boxes of one page of one head.
+bool pool_map(CUtensorMap* m, const dsa_paged_kv* kv, const void* base) {
+  const bool f8 = kv->fmt == DSA_KV_E4M3;
+  const uint64_t e = f8 ? 1 : 2, D = static_cast<uint64_t>(kv->D);
+  const uint32_t cols = static_cast<uint32_t>(std::min<uint64_t>(D, 128 / e));
+  return encode_tiled_4d(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                         {D, static_cast<uint64_t>(kv->page), static_cast<uint64_t>(kv->n_kv), static_cast<uint64_t>(kv->n_pages)},
+                         {D * e, D * e * kv->page, D * e * kv->page * kv->n_kv}, cols, static_cast<uint32_t>(kv->page),
+                         cols * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -123,8 +828,8 @@ using namespace dsa;
 extern "C" {
 
 size_t dsa_paged_attn_workspace(const dsa_paged_kv* kv, const dsa_paged_batch* batch, int n_h, int n_sel) {
-  if (check_paged_host("dsa_paged_attn_workspace", kv, batch, nullptr) != DSA_OK || n_h < 1 || n_sel < 0) return 0;
-  return 16;
+  if (check_paged_host("dsa_paged_attn_workspace", kv, batch, nullptr) != DSA_OK || n_h < 1 || n_h % kv->n_kv || n_sel < 0) return 0;
+  return std::max<size_t>(16, make_plan(kv, batch, n_h, n_sel).total());
 }
 
 dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, const dsa_paged_batch* batch,
@@ -141,19 +846,30 @@ dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, co
   if (inclusive != 0 && inclusive != 1) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: inclusive is 0 or 1");
   if (sel ? n_sel < 1 : n_sel != 0) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: n_sel goes with sel");
   if (n_sel > 1024) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: n_sel <= 1024");
-  if (!(scale > 0.f) || scale > 3.402823466e38f) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: scale must be positive and finite");
-  if (!ws || !aligned16(ws) || ws_bytes < dsa_paged_attn_workspace(kv, batch, n_h, n_sel))
+  if (!(scale > 0.f) || scale > 1e30f) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: scale must be positive and at most 1e30");
+  const Plan pl = make_plan(kv, batch, n_h, n_sel);
+  if (!ws || !aligned16(ws) || ws_bytes < std::max<size_t>(16, pl.total()))
     return set_error(DSA_ERR_WORKSPACE, "dsa_paged_attn: workspace null, misaligned or too small");
-  p.q = q; p.sel = sel; p.n_h = n_h; p.page = kv->page; p.inclusive = inclusive; p.n_sel = n_sel; p.scale = scale;
+  if (pl.units > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: batch too large");
+  p.q = q; p.sel = sel; p.n_h = n_h; p.G = pl.G; p.page = kv->page; p.shift = kv->page == 16 ? 4 : kv->page == 32 ? 5 : kv->page == 64 ? 6 : 7; p.ppt = kTile / kv->page; p.inclusive = inclusive;
+  p.n_sel = n_sel; p.Gx = pl.Gx; p.R = pl.R; p.hbs = pl.hbs; p.max_rb = pl.max_rb; p.tpu = pl.tpu; p.aligned = pl.aligned;
+  p.scale_log2 = scale * kLog2e;
   p.out = out; p.lse = lse;
-  const int G = n_h / kv->n_kv;
-  const int smem = (2 * G * kv->D + G * kTile + 3 * G) * 4;
+  p.err = device_error_word();
+  if (!p.err) return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cannot find the device error word");
+  if (pl.merge) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(w);
+    p.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
+    p.meta = reinterpret_cast<int2*>(w + pl.o_bytes + pl.l_bytes);
+  }
+  CUtensorMap mk, mv;
+  if (!pool_map(&mk, kv, kv->k) || !pool_map(&mv, kv, kv->v))
+    return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cuTensorMapEncodeTiled failed");
   const bool f8 = kv->fmt == DSA_KV_E4M3;
-  auto fn = kv->D == 64 ? (f8 ? paged_attn_simple_kernel<64, true> : paged_attn_simple_kernel<64, false>)
-                        : (f8 ? paged_attn_simple_kernel<128, true> : paged_attn_simple_kernel<128, false>);
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem);
-  if (e == cudaSuccess)
-    e = launch_pdl(fn, dim3(static_cast<unsigned>(batch->total_q * kv->n_kv)), dim3(kTile), smem, static_cast<cudaStream_t>(stream), p);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = kv->D == 64 ? (f8 ? launch_attn<64, true>(mk, mv, p, pl, s) : launch_attn<64, false>(mk, mv, p, pl, s))
+                                    : (f8 ? launch_attn<128, true>(mk, mv, p, pl, s) : launch_attn<128, false>(mk, mv, p, pl, s));
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_paged_attn launch: ") + cudaGetErrorString(e));
   return DSA_OK;
 }

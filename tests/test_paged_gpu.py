@@ -458,7 +458,15 @@ def test_graph_replay_second_stream_and_shared_pages(dsa, fmt, lq):
     q = _bf16(g, 2 * lq, 8, 128).cuda()
     q[lq:] = q[:lq]
     a = dsa.paged_attn(q, kv, both, 0.09, inclusive=True)
-    assert torch.equal(a[:lq], a[lq:])
+    # the two may be cut into parts at different tiles: another order of the
+    # f32 sums, and weights rounded to 8 bits under another maximum, each
+    # within 2^-8 sum p|v| <= 2^-8 max|V| of the exact value, then one rounding
+    most = 2 * 2.0 ** -8 * float(mirror.rows(table[0], 0)[1].nan_to_num().abs().max())
+
+    def near(x, y):
+        torch.testing.assert_close(x.float(), y.float(), rtol=2 * 2.0 ** -8, atol=most)
+
+    near(a[:lq], a[lq:])
     ws = torch.empty(max(16, dsa.paged_attn_workspace(kv, both, 8)), dtype=torch.uint8, device="cuda")
     out = torch.zeros_like(a)
     s = torch.cuda.Stream()
@@ -473,7 +481,8 @@ def test_graph_replay_second_stream_and_shared_pages(dsa, fmt, lq):
         both.start_pos[1] = 100
         graph.replay()
         s.synchronize()
-    assert torch.equal(out[:lq], a[:lq]) and not torch.equal(out[lq:], a[lq:])
+    near(out[:lq], a[:lq])
+    assert not torch.equal(out[lq:], a[lq:])
     assert torch.equal(out, dsa.paged_attn(q, kv, both, 0.09, inclusive=True))
 
 
