@@ -19,10 +19,11 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-s
 
 LIBS = {
     "libdsa.so": ["dsa_api.cu", "indexer_topk.cu", "decode_indexer.cu", "sparse_attn.cu", "noalloc.cu",
-                  "selection_quality.cu", "csa.cu", "lowprec.cu", "paged.cu", "paged_attn.cu"],
+                  "selection_quality.cu", "csa.cu", "lowprec.cu", "paged.cu", "paged_attn.cu",
+                  "paged_prefill.cu"],
     "libdsa_synth.so": ["synth.cu"],
 }
-DEPS = ["dsa_ptx.cuh", "dsa_internal.h", "paged.cuh"]
+DEPS = ["dsa_ptx.cuh", "dsa_internal.h", "paged.cuh", "paged_attn.cuh"]
 
 
 def _stale(out: str, srcs: list[str]) -> bool:

@@ -15,6 +15,7 @@
 #include <string>
 
 #include "paged.cuh"
+#include "paged_attn.cuh"
 
 namespace dsa {
 namespace {
@@ -809,15 +810,20 @@ cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnP
                     : (pl.NH == 16 ? launch_attn<D, F8, 16>(k, v, p, pl, s) : launch_attn<D, F8, 32>(k, v, p, pl, s));
 }
 
+// Many rows that read all pages: query rows on the tile's rows.
+bool use_prefill(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n_sel) {
+  return !n_sel && static_cast<long long>(n_h / kv->n_kv) * pb->max_Lq > 32;
+}
+
 // Tensor map of a pool: {columns, slots, heads, pages}, boxes of one page of one head.
-bool pool_map(CUtensorMap* m, const dsa_paged_kv* kv, const void* base) {
+bool pool_map(CUtensorMap* m, const dsa_paged_kv* kv, const void* base, bool swizzled) {
   const bool f8 = kv->fmt == DSA_KV_E4M3;
   const uint64_t e = f8 ? 1 : 2, D = static_cast<uint64_t>(kv->D);
   const uint32_t cols = static_cast<uint32_t>(std::min<uint64_t>(D, 128 / e));
   return encode_tiled_4d(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
                          {D, static_cast<uint64_t>(kv->page), static_cast<uint64_t>(kv->n_kv), static_cast<uint64_t>(kv->n_pages)},
                          {D * e, D * e * kv->page, D * e * kv->page * kv->n_kv}, cols, static_cast<uint32_t>(kv->page),
-                         cols * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                         !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : cols * e == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
@@ -829,7 +835,9 @@ extern "C" {
 
 size_t dsa_paged_attn_workspace(const dsa_paged_kv* kv, const dsa_paged_batch* batch, int n_h, int n_sel) {
   if (check_paged_host("dsa_paged_attn_workspace", kv, batch, nullptr) != DSA_OK || n_h < 1 || n_h % kv->n_kv || n_sel < 0) return 0;
-  return std::max<size_t>(16, make_plan(kv, batch, n_h, n_sel).total());
+  if (n_h > 128) return 0;
+  return std::max<size_t>(16, use_prefill(kv, batch, n_h, n_sel) ? paged_prefill_plan(kv, batch, n_h).total()
+                                                                 : make_plan(kv, batch, n_h, n_sel).total());
 }
 
 dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, const dsa_paged_batch* batch,
@@ -847,29 +855,44 @@ dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, co
   if (sel ? n_sel < 1 : n_sel != 0) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: n_sel goes with sel");
   if (n_sel > 1024) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: n_sel <= 1024");
   if (!(scale > 0.f) || scale > 1e30f) return set_error(DSA_ERR_INVALID_ARG, "dsa_paged_attn: scale must be positive and at most 1e30");
-  const Plan pl = make_plan(kv, batch, n_h, n_sel);
-  if (!ws || !aligned16(ws) || ws_bytes < std::max<size_t>(16, pl.total()))
+  if (!ws || !aligned16(ws) || ws_bytes < dsa_paged_attn_workspace(kv, batch, n_h, n_sel))
     return set_error(DSA_ERR_WORKSPACE, "dsa_paged_attn: workspace null, misaligned or too small");
-  if (pl.units > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: batch too large");
-  p.q = q; p.sel = sel; p.n_h = n_h; p.G = pl.G; p.page = kv->page; p.shift = kv->page == 16 ? 4 : kv->page == 32 ? 5 : kv->page == 64 ? 6 : 7; p.ppt = kTile / kv->page; p.inclusive = inclusive;
-  p.n_sel = n_sel; p.Gx = pl.Gx; p.R = pl.R; p.hbs = pl.hbs; p.max_rb = pl.max_rb; p.tpu = pl.tpu; p.aligned = pl.aligned;
-  p.scale_log2 = scale * kLog2e;
-  p.out = out; p.lse = lse;
-  p.err = device_error_word();
-  if (!p.err) return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cannot find the device error word");
-  if (pl.merge) {
-    uint8_t* w = static_cast<uint8_t*>(ws);
-    p.part_o = reinterpret_cast<float*>(w);
-    p.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
-    p.meta = reinterpret_cast<int2*>(w + pl.o_bytes + pl.l_bytes);
-  }
-  CUtensorMap mk, mv;
-  if (!pool_map(&mk, kv, kv->k) || !pool_map(&mv, kv, kv->v))
-    return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cuTensorMapEncodeTiled failed");
-  const bool f8 = kv->fmt == DSA_KV_E4M3;
+  unsigned int* err = device_error_word();
+  if (!err) return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cannot find the device error word");
+  const bool f8 = kv->fmt == DSA_KV_E4M3, many = use_prefill(kv, batch, n_h, n_sel);
+  const int shift = kv->page == 16 ? 4 : (kv->page == 32 ? 5 : (kv->page == 64 ? 6 : 7));
+  uint8_t* w = static_cast<uint8_t*>(ws);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = kv->D == 64 ? (f8 ? launch_attn<64, true>(mk, mv, p, pl, s) : launch_attn<64, false>(mk, mv, p, pl, s))
-                                    : (f8 ? launch_attn<128, true>(mk, mv, p, pl, s) : launch_attn<128, false>(mk, mv, p, pl, s));
+  CUtensorMap mk, mv;
+  if (!pool_map(&mk, kv, kv->k, !(many && f8)) || !pool_map(&mv, kv, kv->v, !(many && f8)))
+    return set_error(DSA_ERR_CUDA, "dsa_paged_attn: cuTensorMapEncodeTiled failed");
+  cudaError_t e;
+  if (many) {
+    const PrefillPlan pl = paged_prefill_plan(kv, batch, n_h);
+    if (pl.units * 256 > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: batch too large");
+    PrefillParams x{};
+    x.a = p.a; x.q = q; x.n_h = n_h; x.G = n_h / kv->n_kv; x.page = kv->page; x.shift = shift; x.ppt = kTile / kv->page;
+    x.inclusive = inclusive; x.tok = pl.tok; x.blocks = pl.blocks; x.splits = pl.splits; x.scale_log2 = scale * kLog2e;
+    x.out = out; x.lse = lse; x.err = err;
+    if (pl.splits > 1) {
+      x.part_o = reinterpret_cast<float*>(w);
+      x.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
+    }
+    e = paged_prefill_launch(mk, mv, kv->D, f8, x, s);
+  } else {
+    const Plan pl = make_plan(kv, batch, n_h, n_sel);
+    if (pl.units > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_attn: batch too large");
+    p.q = q; p.sel = sel; p.n_h = n_h; p.G = pl.G; p.page = kv->page; p.shift = shift; p.ppt = kTile / kv->page;
+    p.inclusive = inclusive; p.n_sel = n_sel; p.Gx = pl.Gx; p.R = pl.R; p.hbs = pl.hbs; p.max_rb = pl.max_rb; p.tpu = pl.tpu;
+    p.aligned = pl.aligned; p.scale_log2 = scale * kLog2e; p.out = out; p.lse = lse; p.err = err;
+    if (pl.merge) {
+      p.part_o = reinterpret_cast<float*>(w);
+      p.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
+      p.meta = reinterpret_cast<int2*>(w + pl.o_bytes + pl.l_bytes);
+    }
+    e = kv->D == 64 ? (f8 ? launch_attn<64, true>(mk, mv, p, pl, s) : launch_attn<64, false>(mk, mv, p, pl, s))
+                    : (f8 ? launch_attn<128, true>(mk, mv, p, pl, s) : launch_attn<128, false>(mk, mv, p, pl, s));
+  }
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_paged_attn launch: ") + cudaGetErrorString(e));
   return DSA_OK;
 }

@@ -1,0 +1,632 @@
+// paged_prefill.cu -- attention of many rows of a sequence over all pages of
+// its cache (prompts and chunks of prompts; dsa_paged_attn).
+//
+// Query rows on the 128 rows of the tensor-core tile: a tile holds TOK = 128/G
+// consecutive tokens x the G heads that share a key/value head, a CTA works on
+// two tiles in turn so that one's softmax runs under the other's products:
+//     S[128 rows, 128 keys] = Q K^T,   O[128 rows, D] += P V
+// S and O live in TMEM (all 512 columns); P overwrites S and is the A operand
+// of the second product.  An 8-bit cache is widened to f16 (exact) on its way
+// from a staging tile to the operand tile by four warps of their own; Q rows
+// are scaled to f16 by a power of two per row, so that the products stay exact.
+#include <algorithm>
+
+#include "paged.cuh"
+#include "paged_attn.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kMetas = 8;
+constexpr int kStages = 2;     // staging tiles of an 8-bit cache
+constexpr int kRing = 4;       // operand tiles: K, V, K, V
+constexpr int kSoftWarps = 8, kConvWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 16 * 32;  // four warpgroups, for the register split (two warps idle)
+// 65,536 registers: 128 a thread at launch; 2 x 128 x 208 + 2 x 128 x 48
+constexpr int kSoftRegs = 208, kOtherRegs = 48;
+constexpr float kLazy = 8.f;   // a row's reference exponent may lag its maximum by this much
+
+template <int D, bool F8>
+struct PreCfg {
+  static constexpr int kSlabs = D / 64;               // operand slabs of 64 columns (128 bytes)
+  static constexpr int kSlabBytes = kTile * 128;
+  static constexpr int kEntry = kSlabs * kSlabBytes;  // an operand tile
+  static constexpr int kStage = F8 ? kTile * D : 0;
+  static constexpr int kMetaBytes = kMetas * 8 * 16;
+  static constexpr int kSmem = 1024 + (2 + kRing) * kEntry + kStages * kStage + kMetaBytes +
+                               8 * (2 * kRing + 2 * kStages + kMetas + 9) + 32;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Unit {
+  int b, row0, rows, nq, kvh;     // first packed row, rows of the unit, Q tiles
+  int t0, t1;                     // visible positions of the first and last row
+  int lo, hi[2];                  // key tiles of each Q tile
+};
+
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Adds the values of positions [s0, s1) that are not finite to a row's output
+// (the tiles held zeros in their place, because other rows do not see them).
+template <int D, bool F8>
+__device__ __forceinline__ void add_nonfinite(const PrefillParams& p, int b, int kvh, int s0, int s1, float* part, dsa_bf16* out) {
+  for (int s = s0; s < s1; ++s) {
+    const int pg = paged_page(p.a, b, s / p.page);
+    if (pg < 0) continue;
+    const int64_t va = ((static_cast<int64_t>(pg) * p.a.n_kv + kvh) * p.page + s % p.page) * D;
+    for (int c = 0; c < D; ++c) {
+      float v;
+      if constexpr (F8) v = e4m3x2_to_f32(static_cast<const uint8_t*>(p.a.v)[va + c]).x;
+      else v = __uint_as_float(static_cast<uint32_t>(static_cast<const dsa_bf16*>(p.a.v)[va + c]) << 16);
+      if (fabsf(v) <= 3.4e38f) continue;
+      if (part) part[c] += v;
+      else out[c] = static_cast<dsa_bf16>(pack_bf16(__uint_as_float(static_cast<uint32_t>(out[c]) << 16) + v, 0.f));
+    }
+  }
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
+  using C = PreCfg<D, F8>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* q_smem = smem;
+  uint8_t* ring = q_smem + 2 * C::kEntry;
+  uint8_t* stage = ring + kRing * C::kEntry;
+  float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, 1 / V scale
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(meta) + C::kMetaBytes);
+  uint64_t *full = bars, *empty = full + kRing, *st_full = empty + kRing, *st_empty = st_full + kStages;
+  uint64_t *meta_full = st_empty + kStages, *s_full = meta_full + kMetas, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *q_full = o_full + 1, *v_fixed = q_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_fixed + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* poison = abort_flag + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], F8 ? 4 : 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < kStages; ++i) { mbar_init(&st_full[i], 1); mbar_init(&st_empty[i], 4); }
+    for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); }
+    mbar_init(o_full, 1);
+    mbar_init(q_full, kSoftWarps);
+    mbar_init(&v_fixed[0], 4);
+    mbar_init(&v_fixed[1], 4);
+    *abort_flag = 0;
+    *poison = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  // the unit of this CTA: late blocks first (they see the most keys)
+  Unit u;
+  const int split = blockIdx.x % p.splits;
+  int64_t id = blockIdx.x / p.splits;
+  {
+    const int per = p.a.B * p.a.n_kv;
+    const int blk = p.blocks - 1 - static_cast<int>(id / per);
+    u.kvh = static_cast<int>(id % p.a.n_kv);
+    u.b = static_cast<int>(id % per) / p.a.n_kv;
+    int r0, n;
+    paged_rows(p.a, u.b, r0, n);
+    const int first = blk * 2 * p.tok;
+    u.row0 = r0 + first;
+    u.rows = max(0, min(2 * p.tok, n - first));
+    u.nq = u.rows > p.tok ? 2 : (u.rows > 0 ? 1 : 0);
+    u.t0 = u.t1 = 0;
+    u.lo = u.hi[0] = u.hi[1] = 0;
+    if (u.rows > 0) {
+      u.t0 = paged_visible(p.a, u.b, first, p.inclusive);
+      u.t1 = paged_visible(p.a, u.b, first + u.rows - 1, p.inclusive);
+      const int tq = paged_visible(p.a, u.b, first + min(u.rows, p.tok) - 1, p.inclusive);
+      const int all = (u.t1 + kTile - 1) / kTile, one = (tq + kTile - 1) / kTile;
+      u.lo = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
+      u.hi[1] = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits);
+      u.hi[0] = max(u.lo, min(u.hi[1], one));
+      if (u.nq == 1) u.hi[1] = u.hi[0];
+    }
+  }
+  const int n_tiles = u.hi[1] - u.lo, n0 = u.hi[0] - u.lo;  // tile 1 of Q never sees fewer keys than tile 0
+  const int fix = max(u.lo, u.t0 / kTile) - u.lo;           // from this tile on, V slots need a look
+
+  if (warp >= kSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kTmaWarp) {
+    if (lane == 0) { tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
+    const int per = 32 / p.ppt, n_vis = (u.t1 + p.page - 1) / p.page;
+    const auto fetch = [&](int tile, int& pg, float& ks, float& vs) {
+      const int j = tile * p.ppt + lane;
+      pg = j < n_vis ? paged_page(p.a, u.b, j) : -1;
+      ks = vs = 1.f;
+      if (F8 && pg >= 0) {
+        const int64_t at = static_cast<int64_t>(pg) * p.a.n_kv + u.kvh;
+        ks = __ldg(p.a.k_scale + at);
+        vs = __ldg(p.a.v_scale + at);
+      }
+    };
+    int pg = -1, pn = -1;
+    float ks = 1.f, vs = 1.f, kn = 1.f, vn = 1.f;
+    if (n_tiles > 0) fetch(u.lo, pn, kn, vn);
+    bool ok = true;
+    int i = 0;
+    for (; i < n_tiles && ok; ++i) {
+      const int in = i % per;
+      if (in == 0) {
+        pg = pn; ks = kn; vs = vn;
+        if (i + per < n_tiles) fetch(u.lo + i + per, pn, kn, vn);
+      }
+      const int src = in * p.ppt + lane % p.ppt;
+      const int mp = __shfl_sync(0xffffffffu, pg, src);
+      const float mk = __shfl_sync(0xffffffffu, ks, src), mv = __shfl_sync(0xffffffffu, vs, src);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = 2 * i + kv;
+        constexpr int kDepth = F8 ? kStages : kRing;
+        const int st = e % kDepth;
+        uint64_t *fb = F8 ? &st_full[st] : &full[st], *eb = F8 ? &st_empty[st] : &empty[st];
+        uint8_t* dst = F8 ? stage + st * C::kStage : ring + st * C::kEntry;
+        ok = __all_sync(0xffffffffu, mbar_wait(eb, ((e / kDepth) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (F8 && kv == 0) {
+          if (lane < p.ppt) meta[i % kMetas * 8 + lane] = make_float4(mk, __log2f(mv), __fdividef(1.f, mv), 0.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
+        }
+        if (lane == 0) mbar_arrive_expect_tx(fb, F8 ? C::kStage : C::kEntry);
+        __syncwarp();
+        if (lane < p.ppt) {  // a slot without a page reads outside the pool: zeros
+          const int page = mp >= 0 ? mp : p.a.n_pages;
+          if constexpr (F8) {
+            tma_load_4d(dst + lane * p.page * D, kv ? &tm_v : &tm_k, fb, 0, 0, u.kvh, page);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::kSlabs; ++c)
+              tma_load_4d(dst + c * C::kSlabBytes + lane * p.page * 128, kv ? &tm_v : &tm_k, fb, c * 64, 0, u.kvh, page);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {  // let the loads in flight land
+      constexpr int kDepth = F8 ? kStages : kRing;
+      for (int st = 0; st < kDepth; ++st)
+        for (int w = 0; w < 64 && 2 * i > st; ++w)
+          if (mbar_try_wait(smem_u32(F8 ? &st_full[st] : &full[st]), ((2 * i - 1 - st) / kDepth) & 1)) break;
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t fmt = F8 ? 0u : (1u << 7) | (1u << 10);
+      constexpr uint32_t idesc_qk = (make_idesc_bf16(128, kTile, 0, 0) & ~((1u << 7) | (1u << 10))) | fmt;
+      constexpr uint32_t idesc_pv = (make_idesc_bf16(128, D, 0, 1) & ~((1u << 7) | (1u << 10))) | fmt;
+      const uint32_t qb = smem_u32(q_smem);
+      // descriptors differ in the start address alone (16-byte units, low bits)
+      const uint64_t qd = make_smem_desc(qb, 16, 1024, kSwizzle128B);
+      const uint64_t kd = make_smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+      const uint64_t vd = make_smem_desc(smem_u32(ring), C::kSlabBytes, 1024, kSwizzle128B);
+      const auto qk = [&](int q, int i) {
+        const uint64_t a0 = qd + q * (C::kEntry >> 4), b0 = kd + (2 * i % kRing) * (C::kEntry >> 4);
+#pragma unroll 1
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (C::kSlabBytes >> 4) + (k & 3) * 2;
+          umma_bf16_ss(tmem + q * 128, a0 + off, b0 + off, idesc_qk, k != 0);
+        }
+        umma_commit(&s_full[q]);
+      };
+      const auto pv = [&](int q, int i) {
+        const uint64_t b0 = vd + ((2 * i + 1) % kRing) * (C::kEntry >> 4);
+#pragma unroll 1
+        for (int k = 0; k < kTile / 16; ++k)
+          umma_bf16_ts(tmem + 256 + q * D, tmem + q * 128 + k * 8, b0 + k * (2048 >> 4), idesc_pv, (i | k) != 0);
+      };
+      const auto wait_tile = [&](int e) { return mbar_wait(&full[e % kRing], (e / kRing) & 1, abort_flag); };
+      bool ok = mbar_wait(q_full, 0, abort_flag) && wait_tile(0);
+      if (ok) {
+        tc_fence_after();
+        if (n0 > 0) qk(0, 0);
+        if (u.nq > 1) qk(1, 0);
+        umma_commit(&empty[0]);
+      }
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        const int st = (2 * i + 1) % kRing;
+        for (int q = 0; q < u.nq && ok; ++q) {
+          const int nq = q ? n_tiles : n0;
+          if (i < nq) {
+            ok = mbar_wait(&p_full[q], i & 1, abort_flag);
+            if (q == 0 || i >= n0) {
+              ok = ok && (F8 ? wait_tile(2 * i + 1) : mbar_wait(&v_fixed[i & 1], (i >> 1) & 1, abort_flag));
+            }
+            if (!ok) break;
+            tc_fence_after();
+            pv(q, i);
+          }
+          if (i + 1 < n_tiles) {
+            if (q == 0) {
+              ok = wait_tile(2 * i + 2);
+              tc_fence_after();
+            }
+            if (ok && i + 1 < nq) qk(q, i + 1);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&empty[st]);
+        if (i + 1 < n_tiles) umma_commit(&empty[(2 * i + 2) % kRing]);
+      }
+      if (ok) umma_commit(o_full);
+    }
+  } else if (warp < kTmaWarp) {
+    // ---------------------------------------------------------------- 8-bit tiles to f16; V slots past the rows
+    const int tid = threadIdx.x - kConvWarp * 32;
+    bool ok = true;
+    if constexpr (F8) {
+      for (int e = 0; e < 2 * n_tiles && ok; ++e) {
+        const int st = e % kStages, rg = e % kRing, i = e >> 1;
+        ok = mbar_wait(&st_full[st], (e / kStages) & 1, abort_flag) && mbar_wait(&empty[rg], ((e / kRing) & 1) ^ 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t* src = stage + st * C::kStage;
+        uint8_t* dst = ring + rg * C::kEntry;
+        const bool look = (e & 1) && i >= fix;
+        constexpr int kChunks = D / 16;  // 16-byte chunks of a staged row
+#pragma unroll 2
+        for (int j = 0; j < kTile * kChunks / 128; ++j) {
+          const int c = j * 128 + tid, row = c / kChunks, cc = c % kChunks;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + c * 16);
+          uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          if (look) {
+            const int pos = (u.lo + i) * kTile + row;
+            if (pos >= u.t0) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const uint32_t nan = __vcmpeq4(x[v] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                if (nan && pos < u.t1) *poison = 1;
+                x[v] = pos < u.t1 ? x[v] & ~nan : 0u;
+              }
+            }
+          }
+          uint32_t y[8];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            y[2 * v] = f16x2_of_e4m3x2(x[v] & 0xffffu);
+            y[2 * v + 1] = f16x2_of_e4m3x2(x[v] >> 16);
+          }
+          uint8_t* d = dst + cc / 4 * C::kSlabBytes + row * 128;
+          const int ch = cc % 4 * 2;
+          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&st_empty[st]);
+          mbar_arrive(&full[rg]);
+        }
+      }
+    } else {
+      for (int i = 0; i < n_tiles && ok; ++i) {  // every V tile passes here, so that the phases stay in step
+        const int e = 2 * i + 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[e % kRing], (e / kRing) & 1, abort_flag));
+        if (!ok) break;
+        const int pos = (u.lo + i) * kTile + tid;
+        if (i >= fix && pos >= u.t0) {
+#pragma unroll
+          for (int c = 0; c < C::kSlabs; ++c) {
+            uint4* row = reinterpret_cast<uint4*>(ring + e % kRing * C::kEntry + c * C::kSlabBytes + tid * 128);
+            for (int v = 0; v < 8; ++v) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (pos < u.t1) {
+                w = row[v];
+                uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t inf = __vcmpeq2(y[k] & 0x7f807f80u, 0x7f807f80u);
+                  if (inf) *poison = 1;
+                  y[k] &= ~inf;
+                }
+                w = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+              row[v] = w;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_fixed[i & 1]);
+      }
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ---------------------------------------------------------------- softmax (thread = row) and output
+    const int q = warp >> 2, m = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + q * 128 + lanes, to = tmem + 256 + q * D + lanes;
+    const int tok = m / p.G, g = m - tok * p.G;
+    const int row = q * p.tok + tok;               // row of the unit
+    const bool live = tok < p.tok && row < u.rows;
+    const int t = live ? paged_visible(p.a, u.b, u.row0 - __ldg(p.a.cu_q + u.b) + row, p.inclusive) : 0;
+    const int64_t at = static_cast<int64_t>(u.row0 + row) * p.n_h + u.kvh * p.G + g;
+    float cr = p.scale_log2;  // factor of the row's scores
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * D);
+      uint8_t* dst = q_smem + q * C::kEntry + m * 128;
+      float mul = 1.f;
+      if constexpr (F8) {  // X = the power of two with 2^-1 X < amax <= X
+        float amax = 0.f;
+        for (int c = 0; c < D / 8; ++c) {
+          float f[8];
+          bf16x8_to_f32(live ? __ldg(src + c) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+        }
+        const uint32_t w = __float_as_uint(fminf(amax, 3.3e38f));
+        const int ex = min(max(static_cast<int>(w >> 23) - 127 + ((w & 0x7fffffu) ? 1 : 0), -100), 126);
+        mul = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        cr *= __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      }
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        if constexpr (F8) {
+          float f[8];
+          bf16x8_to_f32(w, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = fabsf(f[e]) <= 3.4e38f ? f[e] * mul : __int_as_float(0x7fffffff);
+          w = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+        }
+        *reinterpret_cast<uint4*>(dst + c / 8 * C::kSlabBytes + ((c % 8 ^ (m & 7)) << 4)) = w;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+
+    float ref = -INFINITY, l = 0.f;  // reference exponent, sum of 2^(score - ref)
+    const int nt = q ? (u.nq > 1 ? n_tiles : 0) : n0;
+    bool ok = true;
+    for (int i = 0; i < nt && ok; ++i) {
+      const int lim = t - (u.lo + i) * kTile;  // keys of the tile that the row sees
+      const bool edge = __any_sync(0xffffffffu, lim < kTile);
+      if (F8) ok = mbar_wait(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag);
+      ok = mbar_wait(&s_full[q], i & 1, abort_flag) && ok;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* mt = meta + i % kMetas * 8;
+      bool find = __any_sync(0xffffffffu, ref == -INFINITY && lim > 0);
+      uint32_t pk[64];
+      float sum;
+      while (true) {
+        if (find) {  // the rows' maxima first
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32<32>(ts + c * 32, s);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float part = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                part = fmaxf(part, !edge || c * 32 + h * 16 + e < lim ? __uint_as_float(s[h * 16 + e]) : -INFINITY);
+              if constexpr (F8) {
+                const float4 sc = mt[(c * 32 + h * 16) >> p.shift];
+                part = part == -INFINITY ? part : fmaf(part, cr * sc.x, sc.y);
+              } else {
+                part *= cr;
+              }
+              top = fmaxf(top, part);
+            }
+          }
+          const float next = fmaxf(ref, top);
+          const float f = next == ref ? 1.f : ex2_approx(ref - next);
+          ref = next;
+          l *= f;
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // O of the tiles before is complete (products finish in order)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32<32>(to + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32x32(to + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float mu = ref == -INFINITY ? 0.f : ref;
+        float high = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tmem_ld32<32>(ts + c * 32, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float k = cr, add = -mu, inv = 1.f;
+            if constexpr (F8) {
+              const float4 sc = mt[(c * 32 + h * 16) >> p.shift];
+              k = cr * sc.x;
+              add = sc.y - mu;
+              inv = sc.z;
+            }
+            float x[16], part = 0.f, big = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              x[e] = fmaf(__uint_as_float(s[h * 16 + e]), k, add);
+              if (edge && c * 32 + h * 16 + e >= lim) x[e] = -INFINITY;
+              big = fmaxf(big, x[e]);
+            }
+            high = fmaxf(high, big);
+            float w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = ex2_approx(x[e]);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              part += w[e] + w[e + 1];
+              pk[c * 16 + h * 8 + e / 2] = F8 ? pack_f16(w[e], w[e + 1]) : pack_bf16(w[e], w[e + 1]);
+            }
+            if constexpr (F8) {
+              // weights that the V scale makes tiny, but not their share of the sum
+              if (big < -60.f && big > -INFINITY) {
+                part = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) part += ex2_approx(x[e] - (add + mu));
+              } else {
+                part *= inv;
+              }
+            }
+            sum += part;
+          }
+        }
+        if (!__any_sync(0xffffffffu, high > kLazy)) break;
+        find = true;
+      }
+      l += sum;
+      tmem_st32x32(ts, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+      tmem_st32x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[q]);
+    }
+    // ---- output
+    if (ok && nt > 0) ok = mbar_wait(o_full, 0, abort_flag);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && q < u.nq) {
+      tc_fence_after();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float l2 = l == 0.f ? -INFINITY : ref + log2f(l);
+      const int64_t part = ((id * p.splits + split) * 2 + q) * 128 + m;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tmem_ld32<32>(to + c * 32, o);
+          tmem_ld_wait();
+        }
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = nt > 0 && l != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+        if (!live) continue;
+        if (p.splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16(y[8 * e], y[8 * e + 1]), pack_bf16(y[8 * e + 2], y[8 * e + 3]),
+                                pack_bf16(y[8 * e + 4], y[8 * e + 5]), pack_bf16(y[8 * e + 6], y[8 * e + 7]));
+        }
+      }
+      if (live) {
+        if (p.splits > 1) p.part_l[part] = l2;
+        else if (p.lse) p.lse[at] = l2 == -INFINITY ? -INFINITY : l2 * 0.6931471805599453f;
+        if (*poison)
+          add_nonfinite<D, F8>(p, u.b, u.kvh, max(u.t0, u.lo * kTile), min(t, u.hi[1] * kTile), p.splits > 1 ? p.part_o + part * D : nullptr,
+                               p.out + at * D);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.err, 1u);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of split rows: one block per (unit, Q tile, 128 / (D/4) rows).
+template <int D>
+__global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillParams p) {
+  constexpr int kVecs = D / 4, kRows = 128 / kVecs;
+  pdl_trigger();
+  pdl_wait();
+  const int per = p.a.B * p.a.n_kv;
+  const int64_t tile = blockIdx.x / (128 / kRows), id = tile / 2;
+  const int q = static_cast<int>(tile & 1), m = blockIdx.x % (128 / kRows) * kRows + threadIdx.x / kVecs, v = threadIdx.x % kVecs;
+  const int blk = p.blocks - 1 - static_cast<int>(id / per), kvh = static_cast<int>(id % p.a.n_kv);
+  const int b = static_cast<int>(id % per) / p.a.n_kv;
+  int r0, n;
+  paged_rows(p.a, b, r0, n);
+  const int tok = m / p.G, row = blk * 2 * p.tok + q * p.tok + tok;
+  if (tok >= p.tok || row >= n) return;
+  const auto at = [&](int s) { return ((id * p.splits + s) * 2 + q) * 128 + m; };
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_l[at(s)]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float l2 = p.part_l[at(s)], w = exp2f(l2 - ref);
+    sum += w;
+    if (l2 == -INFINITY) continue;
+    const float4 o = *reinterpret_cast<const float4*>(p.part_o + at(s) * D + v * 4);
+    acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t o = static_cast<int64_t>(r0 + row) * p.n_h + kvh * p.G + (m - tok * p.G);
+  *reinterpret_cast<uint2*>(p.out + o * D + v * 4) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (v == 0 && p.lse) p.lse[o] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, bool F8>
+cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PrefillParams& p, cudaStream_t s) {
+  using C = PreCfg<D, F8>;
+  const int64_t units = static_cast<int64_t>(p.blocks) * p.a.B * p.a.n_kv;
+  auto fn = paged_prefill_kernel<D, F8>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), C::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(fn, dim3(static_cast<unsigned>(units * p.splits)), dim3(kThreads), C::kSmem, s, k, v, p);
+  if (e == cudaSuccess && p.splits > 1)
+    e = launch_pdl(paged_prefill_merge_kernel<D>, dim3(static_cast<unsigned>(units * 2 * (128 / (512 / D)))), dim3(128), 0, s, p);
+  return e;
+}
+
+}  // namespace
+
+PrefillPlan paged_prefill_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h) {
+  PrefillPlan pl{};
+  const int G = n_h / kv->n_kv;
+  pl.tok = 128 / G;
+  pl.blocks = (pb->max_Lq + 2 * pl.tok - 1) / (2 * pl.tok);
+  const int64_t units = static_cast<int64_t>(pl.blocks) * pb->B * kv->n_kv;
+  pl.units = units;
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 148;
+  const int tiles = (pb->max_Lk + kTile - 1) / kTile;
+  pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, tiles / 8)));
+  if (pl.splits > 1) {
+    pl.o_bytes = static_cast<size_t>(units) * pl.splits * 256 * kv->D * 4;
+    pl.l_bytes = static_cast<size_t>(units) * pl.splits * 256 * 4;
+  }
+  return pl;
+}
+
+cudaError_t paged_prefill_launch(const CUtensorMap& k, const CUtensorMap& v, int D, bool f8, const PrefillParams& p, cudaStream_t s) {
+  return D == 64 ? (f8 ? launch<64, true>(k, v, p, s) : launch<64, false>(k, v, p, s))
+                 : (f8 ? launch<128, true>(k, v, p, s) : launch<128, false>(k, v, p, s));
+}
+
+}  // namespace dsa
