@@ -613,6 +613,7 @@ class PagedKV:
         self.desc = PagedKVDesc(n, page, h, D, fmt, *[None if t is None else t.data_ptr() for t in
                                                       (k, v, k_scale, v_scale, sum, sum_scale)])
         self.ref = ctypes.byref(self.desc)
+        self.device = k.get_device()
 
     @classmethod
     def empty(cls, n_pages: int, page: int, n_kv: int, D: int, *, fmt: str = "e4m3", summaries: bool = True,
@@ -651,6 +652,7 @@ class PagedBatch:
         self.desc = PagedBatchDesc(B, cu_q.data_ptr(), start_pos.data_ptr(), block_table.data_ptr(), max_pages,
                                    total_q, max_Lq, max_Lk)
         self.ref = ctypes.byref(self.desc)
+        self.device = block_table.get_device()
 
     @classmethod
     def from_lens(cls, q_lens, start_pos, block_table):
@@ -680,37 +682,45 @@ def _same_device(*tensors):
 
 
 class _on:
-    """Makes a tensor's device current for a call and gives its stream."""
+    """Makes a device current for a call and gives its current stream's handle."""
 
-    def __init__(self, t):
-        self.dev = t.device
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
         import torch
-        self.old = torch.cuda.current_device()
-        if self.old != self.dev.index:
-            torch.cuda.set_device(self.dev)
-        return ctypes.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+        self.old = torch._C._cuda_getDevice()
+        if self.old != self.index:
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        import torch
-        if self.old != self.dev.index:
+        if self.old != self.index:
+            import torch
             torch.cuda.set_device(self.old)
 
 
-def _token_rows(t, name, rows, heads, D):
+def _dense(t, dtype, shape, dev, name):
+    """_need, for a decode step's short calls: the fast path is one line.
+    Returns the address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _need(t, dtype, shape, name)
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _token_rows(t, dev, name, rows, heads, D):
     """A [rows, heads, D] bf16 tensor whose rows may be strided (a slice of a
     fused projection).  Returns the row stride in elements."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads or 'n_h', D)}")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        raise TypeError(f"{name} must be {torch.bfloat16} on cuda:{dev}, got {t.dtype} on {t.device}")
+    if t.shape != (rows, heads, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, D)}")
+    row, head, col = t.stride()
+    if col != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: the heads and columns of a row must be contiguous")
-    return t.stride(0) if rows > 1 else t.shape[1] * D
+    return row if rows > 1 else heads * D
 
 
 def paged_append(kv: PagedKV, batch: PagedBatch, k, v, cos=None, sin=None, *, q=None, interleaved: bool = False,
@@ -721,31 +731,43 @@ def paged_append(kv: PagedKV, batch: PagedBatch, k, v, cos=None, sin=None, *, q=
     dsa_paged_append.  Row strides are free.  Returns the rotated queries
     (q_out) or None."""
     import torch
-    d = kv.desc
-    rows = batch.desc.total_q
-    ks, vs = _token_rows(k, "k", rows, d.n_kv, d.D), _token_rows(v, "v", rows, d.n_kv, d.D)
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    n_pos = rot = 0
-    if cos is not None:
-        _need(cos, torch.float32, name="cos")
-        _need(sin, torch.float32, cos.shape, "sin")
-        if cos.dim() != 2:
-            raise ValueError("cos must be [n_pos, rot/2]")
-        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
-    n_h = qs = 0
+    d, dev = kv.desc, kv.device
+    rows, D, n_kv = batch.desc.total_q, d.D, d.n_kv
+    ks, vs = _token_rows(k, dev, "k", rows, n_kv, D), _token_rows(v, dev, "v", rows, n_kv, D)
+    n_pos = rot = n_h = qs = 0
+    pc = ps = pq = po = None
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2:
+            raise ValueError("cos and sin go together, [n_pos, rot/2] each")
+        n_pos, half = cos.shape
+        pc, ps = _dense(cos, torch.float32, (n_pos, half), dev, "cos"), _dense(sin, torch.float32, (n_pos, half), dev, "sin")
+        rot = 2 * half
     if q is not None:
-        qs, n_h = _token_rows(q, "q", rows, None, d.D), q.shape[1]
+        if q.dim() != 3:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', D)}")
+        n_h = q.shape[1]
+        qs, pq = _token_rows(q, dev, "q", rows, n_h, D), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((rows, n_h, d.D), dtype=torch.bfloat16, device=q.device)
-        _need(q_out, torch.bfloat16, (rows, n_h, d.D), "q_out")
+            q_out = torch.empty((rows, n_h, D), dtype=torch.bfloat16, device=q.device)
+        po = _dense(q_out, torch.bfloat16, (rows, n_h, D), dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    _same_device(kv.k, batch.cu_q, k, v, cos, sin, q, q_out)
-    with _on(kv.k) as stream:
-        _check(lib().dsa_paged_append(kv.ref, batch.ref, _ptr(k), ks, _ptr(v), vs, _ptr(cos), _ptr(sin), n_pos, rot,
-                                      int(interleaved), _ptr(q), qs, n_h, _ptr(q_out), stream))
+    _on_cache(batch, dev)
+    with _on(dev) as stream:
+        _check(lib().dsa_paged_append(kv.ref, batch.ref, k.data_ptr(), ks, v.data_ptr(), vs, pc, ps, n_pos, rot,
+                                      int(interleaved), pq, qs, n_h, po, stream))
     return q_out
+
+
+def _on_cache(batch, dev):
+    if batch.device != dev:
+        raise ValueError(f"the batch is on cuda:{batch.device}, the cache on cuda:{dev}")
+
+
+def _queries(q, rows, D):
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', D)}")
+    return q.shape[1]
 
 
 def page_topk(q, kv: PagedKV, batch: PagedBatch, n_sel: int, *, n_first: int = 1, n_last: int = 1,
@@ -754,23 +776,22 @@ def page_topk(q, kv: PagedKV, batch: PagedBatch, n_sel: int, *, n_first: int = 1
     dsa_page_topk.  q [total_q, n_h, D] bf16 (rotated); returns sel [total_q,
     n_kv, n_sel] int32 (ascending page numbers, then -1)."""
     import torch
-    d = kv.desc
-    rows = batch.desc.total_q
-    _need(q, torch.bfloat16, name="q")
-    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d.D:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', d.D)}")
+    d, dev = kv.desc, kv.device
+    rows, D = batch.desc.total_q, d.D
+    n_h = _queries(q, rows, D)
+    pq = _dense(q, torch.bfloat16, (rows, n_h, D), dev, "q")
     if out is None:
         out = torch.empty((rows, d.n_kv, n_sel), dtype=torch.int32, device=q.device)
-    _need(out, torch.int32, (rows, d.n_kv, n_sel), "out")
-    _same_device(kv.k, batch.cu_q, q, out)
-    with _on(q) as stream:
-        _check(lib().dsa_page_topk(_ptr(q), q.shape[1], kv.ref, batch.ref, int(inclusive), n_sel, n_first, n_last,
-                                   _ptr(out), stream))
+    po = _dense(out, torch.int32, (rows, d.n_kv, n_sel), dev, "out")
+    _on_cache(batch, dev)
+    with _on(dev) as stream:
+        _check(lib().dsa_page_topk(pq, n_h, kv.ref, batch.ref, int(inclusive), n_sel, n_first, n_last, po, stream))
     return out
 
 
 def paged_attn_workspace(kv: PagedKV, batch: PagedBatch, n_h: int, n_sel: int = 0) -> int:
-    return int(lib().dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel))
+    with _on(kv.device):
+        return int(lib().dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel))
 
 
 def paged_attn(q, kv: PagedKV, batch: PagedBatch, scale: float, *, sel=None, inclusive: bool = False, out=None,
@@ -780,26 +801,28 @@ def paged_attn(q, kv: PagedKV, batch: PagedBatch, scale: float, *, sel=None, inc
     Returns out [total_q, n_h, D] bf16 (and fills lse [total_q, n_h] f32 if
     given); see dsa_paged_attn."""
     import torch
-    d = kv.desc
-    rows = batch.desc.total_q
-    _need(q, torch.bfloat16, name="q")
-    if q.dim() != 3 or q.shape[0] != rows or q.shape[2] != d.D:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected {(rows, 'n_h', d.D)}")
-    n_h, n_sel = q.shape[1], 0
+    d, dev = kv.desc, kv.device
+    rows, D = batch.desc.total_q, d.D
+    n_h, n_sel, pl, psel = _queries(q, rows, D), 0, None, None
+    pq = _dense(q, torch.bfloat16, (rows, n_h, D), dev, "q")
     if sel is not None:
         n_sel = sel.shape[-1]
-        _need(sel, torch.int32, (rows, d.n_kv, n_sel), "sel")
+        psel = _dense(sel, torch.int32, (rows, d.n_kv, n_sel), dev, "sel")
     if out is None:
-        out = torch.empty((rows, n_h, d.D), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, (rows, n_h, d.D), "out")
+        out = torch.empty((rows, n_h, D), dtype=torch.bfloat16, device=q.device)
+    po = _dense(out, torch.bfloat16, (rows, n_h, D), dev, "out")
     if lse is not None:
-        _need(lse, torch.float32, (rows, n_h), "lse")
-    _same_device(kv.k, batch.cu_q, q, sel, out, lse, ws)
-    with _on(q) as stream:
+        pl = _dense(lse, torch.float32, (rows, n_h), dev, "lse")
+    _on_cache(batch, dev)
+    with _on(dev) as stream:
+        L = lib()
         if ws is None:
-            ws = torch.empty(max(paged_attn_workspace(kv, batch, n_h, n_sel), 16), dtype=torch.uint8, device=q.device)
-        _check(lib().dsa_paged_attn(_ptr(q), n_h, kv.ref, batch.ref, int(inclusive), _ptr(sel), n_sel, float(scale),
-                                    _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), stream))
+            ws = torch.empty(max(L.dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel), 16), dtype=torch.uint8,
+                             device=q.device)
+        elif not ws.is_contiguous() or ws.get_device() != dev:
+            raise ValueError(f"ws must be contiguous on cuda:{dev}")
+        _check(L.dsa_paged_attn(pq, n_h, kv.ref, batch.ref, int(inclusive), psel, n_sel, scale, po, pl, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), stream))
     return out
 
 
@@ -808,6 +831,7 @@ def check_paged(kv: PagedKV, batch: PagedBatch) -> int:
     contract (checked on the device).  Synchronises the current stream."""
     import torch
     bad = torch.empty(1, dtype=torch.int32, device=batch.cu_q.device)
-    with _on(bad) as stream:
+    _on_cache(batch, kv.device)
+    with _on(kv.device) as stream:
         _check(lib().dsa_check_paged(kv.ref, batch.ref, _ptr(bad), stream))
     return int(bad.item())
