@@ -183,7 +183,7 @@ struct Cfg {
   static constexpr int kWm = kGroups * 2 * 4 * (kHG + 4);
   static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
   static constexpr int kSmem = 1024 + kRing * kEntry + kQBytes + 2 * kPBytes + kMetaBytes + kWm * 4 + 2 * NH * 4 +
-                               4 * NH * 4 + 8 * (2 * kRing + kMetas + 8) + 64;
+                               4 * NH * 4 + kEpiWarps * 4 * kHG * 4 + 8 * (2 * kRing + kMetas + 8) + 64;
   static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
 };
 
@@ -213,7 +213,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   float* wm = reinterpret_cast<float*>(meta + kMetas * 8);        // [group][2][4 warps][HG + 4]
   float* cq = wm + C::kWm;                                        // [2][NH] factor of a head's scores
   float* lsum = cq + 2 * NH;                                      // [4 warps][NH]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(lsum + 4 * NH);
+  float* bcast = lsum + 4 * NH;                                   // [warps][4][HG]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bcast + C::kEpiWarps * 4 * HG);
   uint64_t *full = bars, *empty = full + kRing, *meta_full = empty + kRing;
   uint64_t *s_full = meta_full + kMetas, *p_full = s_full + 2, *pv_done = p_full + 2, *q_full = pv_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 1);
@@ -371,6 +372,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int gh = grp * HG;  // first head of the group
     float* wmg = wm + grp * 2 * 4 * (HG + 4);
+    float* bc = bcast + warp * 4 * HG;  // per warp: references, weight factors, factors of the sums and of O
     int it = 0, seg = 0;
     bool ok = true;
 
@@ -428,19 +430,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (more) load_q(s, 0);
     else if (p.part_l && threadIdx.x < NH) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;  // no part of any unit
     while (ok && more) {
-      float m[HG], mp[HG], l[HG];  // reference exponents of the weights and of the weighted V scales; sums
+      // lane h (mod HG) keeps the reference exponents of head h: m of the
+      // weights, mp of the weighted V scales; every thread its keys' sums
+      float m = -INFINITY, mp = -INFINITY, l[HG];
 #pragma unroll
-      for (int h = 0; h < HG; ++h) { m[h] = -INFINITY; mp[h] = -INFINITY; l[h] = 0.f; }
+      for (int h = 0; h < HG; ++h) l[h] = 0.f;
       const int heads = min(p.Gx, p.G - s.h0);
-      if (F8) ok = mbar_wait(q_full, seg & 1, abort_flag);  // the head factors of this segment are written
+      float c[HG];  // factors of the scores
+      if constexpr (F8) {
+        ok = mbar_wait(q_full, seg & 1, abort_flag);
+#pragma unroll
+        for (int h = 0; h < HG; ++h) c[h] = cq[(seg & 1) * NH + gh + h];
+      }
       for (int i = s.lo; i < s.hi; ++i, ++it) {
         const int buf = it & 1;
         ok = mbar_wait(&meta_full[it % kMetas], (it / kMetas) & 1, abort_flag) && ok;
         const int4 mt = ok ? meta[it % kMetas * 8 + (key >> p.shift)] : make_int4(kNoPage, 0, 0, 0);
         const float ks = __int_as_float(mt.y), vs = __int_as_float(mt.z);
         const int pos = mt.x + (key & (p.page - 1)), past = pos - s.t0;
-        // head row n sees this key from n = nmin on (rows see one position more each)
-        const int nmin = past < 0 ? 0 : (past < s.nr ? (past + 1) * heads : kNoPage);
         float x[HG];
         float lvs = 0.f;
         if constexpr (F8) lvs = __log2f(warp_max_f32(vs));
@@ -454,71 +461,62 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           tmem_ld32<HG>(ts + NH + gh, b);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const float v = fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) * (ks * cq[(seg & 1) * NH + gh + h]);
-            x[h] = gh + h >= nmin ? v : -INFINITY;
-          }
+          for (int h = 0; h < HG; ++h) x[h] = fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) * (ks * c[h]);
         } else {
           uint32_t a[HG];
           tmem_ld32<HG>(ts + gh, a);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < HG; ++h) x[h] = gh + h >= nmin ? __uint_as_float(a[h]) * p.scale_log2 : -INFINITY;
+          for (int h = 0; h < HG; ++h) x[h] = __uint_as_float(a[h]) * p.scale_log2;
+        }
+        const bool edge = __any_sync(0xffffffffu, past >= 0);
+        if (edge) {
+          // head row n sees this key from n = nmin on (rows see one position more each)
+          const int nmin = past < 0 ? 0 : (past < s.nr ? (past + 1) * heads : kNoPage);
+#pragma unroll
+          for (int h = 0; h < HG; ++h) x[h] = gh + h >= nmin ? x[h] : -INFINITY;
         }
         // ---- the tile's maximum per head, over the four warps
         {
           float* w = wmg + (buf * 4 + wq) * (HG + 4);
-          float v = F8 ? lvs : 0.f;
+          float r[HG];
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            const float r = warp_max_f32(x[h]);
-            if (lane == h) v = r;
+          for (int h = 0; h < HG; ++h) r[h] = warp_max_f32(x[h]);
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < HG; h += 4) *reinterpret_cast<float4*>(w + h) = make_float4(r[h], r[h + 1], r[h + 2], r[h + 3]);
+            if (F8) w[HG] = lvs;
           }
-          if (lane <= HG) w[lane] = v;
         }
         if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
-        bool grew = false;
-        float fo[HG];
+        bool grew, grew_l;
         {
           const float* w = wmg + buf * 4 * (HG + 4);
+          const int h = lane % HG;
+          float t = -INFINITY, tp = -INFINITY;
 #pragma unroll
-          for (int h0 = 0; h0 < HG; h0 += 4) {
-            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, tp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 y = *reinterpret_cast<const float4*>(w + q * (HG + 4) + h0);
-              const float yy[4] = {y.x, y.y, y.z, y.w};
-              const float lv = F8 ? w[q * (HG + 4) + HG] : 0.f;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                t[e] = fmaxf(t[e], yy[e]);
-                if (F8) tp[e] = fmaxf(tp[e], yy[e] + lv);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int h = h0 + e;
-              const float mn = fmaxf(m[h], ceilf(t[e]));
-              if (mn > m[h]) {
-                const float f = ex2_approx(m[h] - mn);
-                l[h] *= f;
-                fo[h] = f;
-                m[h] = mn;
-                if (!F8) grew = true;
-              } else {
-                fo[h] = 1.f;
-              }
-              if constexpr (F8) {
-                const float pn = fmaxf(mp[h], ceilf(tp[e]));
-                fo[h] = 1.f;
-                if (pn > mp[h]) {
-                  fo[h] = ex2_approx(mp[h] - pn);
-                  mp[h] = pn;
-                  grew = true;
-                }
-              }
-            }
+          for (int q = 0; q < 4; ++q) {
+            const float y = w[q * (HG + 4) + h];
+            t = fmaxf(t, y);
+            if (F8) tp = fmaxf(tp, y + w[q * (HG + 4) + HG]);
           }
+          const float mn = fmaxf(m, ceilf(t)), pn = F8 ? fmaxf(mp, ceilf(tp)) : mn;
+          const float mu = mn == -INFINITY ? 0.f : mn, mpu = pn == -INFINITY ? 0.f : pn;
+          grew_l = __any_sync(0xffffffffu, mn > m);
+          grew = F8 ? __any_sync(0xffffffffu, pn > mp) : grew_l;
+          if (lane < HG) {
+            bc[lane] = mu;
+            if (F8) bc[HG + lane] = ex2_approx(fminf(mu - mpu + 8.f, 120.f));
+            if (grew_l) bc[2 * HG + lane] = mn > m ? ex2_approx(m - mn) : 1.f;
+            if (F8 && grew) bc[3 * HG + lane] = pn > mp ? ex2_approx(mp - pn) : 1.f;
+          }
+          m = mn;
+          mp = pn;
+          __syncwarp();
+        }
+        if (grew_l) {
+#pragma unroll
+          for (int h = 0; h < HG; ++h) l[h] *= bc[2 * HG + h];
         }
         // ---- weights, as the MMA's B operand.  P(it - 2) has been read.
         if (it >= 2) ok = mbar_wait(&pv_done[buf], ((it - 2) >> 1) & 1, abort_flag) && ok;
@@ -529,10 +527,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float mu = m[h + e] == -INFINITY ? 0.f : m[h + e], mpu = mp[h + e] == -INFINITY ? 0.f : mp[h + e];
-              const float pw = ex2_approx(x[h + e] - mu);
+              const float pw = ex2_approx(x[h + e] - bc[h + e]);
               l[h + e] += pw;
-              w[e] = pw * (vs * ex2_approx(fminf(mu - mpu + 8.f, 120.f)));
+              w[e] = pw * (vs * bc[HG + h + e]);
             }
             const uint32_t hi = e4m3x2(w[0], w[1]);
             const float2 back = e4m3x2_to_f32(hi);
@@ -548,8 +545,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             float w[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float mu = m[h + e] == -INFINITY ? 0.f : m[h + e];
-              w[e] = ex2_approx(x[h + e] - mu);
+              w[e] = ex2_approx(x[h + e] - bc[h + e]);
               l[h + e] += w[e];
             }
             const uint32_t two = pack_bf16(w[0], w[1]);
@@ -565,6 +561,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           tc_fence_after();
           if (wq * 32 < D) {
             constexpr int kParts = F8 && HG == 16 ? 2 : 1;
+            const float* fo = bc + (F8 ? 3 : 2) * HG;
 #pragma unroll
             for (int c = 0; c < kParts; ++c) {
               uint32_t o[16];
@@ -581,7 +578,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // ---- slots that no row of the unit sees hold anything: V = 0 there.
         // A slot that only later rows see must not reach the earlier ones
         // through 0 * inf: such values are set aside and added at the end.
-        if (grp == 0 && __any_sync(0xffffffffu, past >= 0 && mt.x != kNoPage)) {
+        if (grp == 0 && edge && __any_sync(0xffffffffu, past >= 0 && mt.x != kNoPage)) {
           const int e = 2 * it + 1, st = e % kRing;
           ok = mbar_wait(&full[st], (e / kRing) & 1, abort_flag) && ok;
           if (ok && past >= 0 && mt.x != kNoPage) {
@@ -650,11 +647,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int h = 0; h < HG; ++h) o[h] = any ? __uint_as_float(a[h]) : 0.f;
       }
       tc_fence_before();
+      if (lane < HG) {  // head h: the reference of its sum, and what turns O into weights of that reference
+        bc[lane] = m == -INFINITY ? 0.f : m;
+        bc[HG + lane] = F8 ? ex2_approx((mp == -INFINITY ? 0.f : mp) - (m == -INFINITY ? 0.f : m) - 8.f) : 1.f;
+      }
+      __syncwarp();
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
         const float* t = lsum + gh + h;
         l[h] = (t[0] + t[NH]) + (t[2 * NH] + t[3 * NH]);
-        const float f = F8 ? ex2_approx((mp[h] == -INFINITY ? 0.f : mp[h]) - (m[h] == -INFINITY ? 0.f : m[h]) - 8.f) : 1.f;
+        const float f = bc[HG + h];
         o[h] = l[h] == 0.f ? 0.f : o[h] * f / l[h];
       }
       if (poison[seg & 1] && key < D) {  // values that are not finite, for the rows that see them
@@ -681,7 +683,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               const int64_t at = static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads);
               const __nv_bfloat16 y = __float2bfloat16_rn(o[h]);
               p.out[at * D + key] = *reinterpret_cast<const dsa_bf16*>(&y);
-              if (key == 0 && p.lse) p.lse[at] = l[h] == 0.f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
+              if (key == 0 && p.lse) p.lse[at] = l[h] == 0.f ? -INFINITY : (bc[h] + log2f(l[h])) * kLn2;
             }
           }
         }
@@ -691,7 +693,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int h = 0; h < HG; ++h) {
             p.part_o[(slot * NH + gh + h) * D + key] = o[h];
-            if (key == 0) p.part_l[slot * NH + gh + h] = l[h] == 0.f ? -INFINITY : m[h] + log2f(l[h]);
+            if (key == 0) p.part_l[slot * NH + gh + h] = l[h] == 0.f ? -INFINITY : bc[h] + log2f(l[h]);
           }
         }
       }
