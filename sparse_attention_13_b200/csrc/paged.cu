@@ -66,6 +66,7 @@ struct AppendParams {
   int n_h, half, interleaved, n_pos;
   int touched;     // pages a sequence can touch
   int64_t units;   // blocks of cache pages; the blocks after them rotate q
+  int q_runs, q_heads;  // runs of heads a row is cut into, heads of a run
 };
 
 constexpr int kAppendThreads = 256;
@@ -142,23 +143,60 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   pdl_wait();
   const int vec = threadIdx.x % kVecs, g = threadIdx.x / kVecs, c = vec * 8;
 
-  if (blockIdx.x >= p.units) {  // queries: 8 columns of a head per thread
-    const int per_row = p.n_h * kVecs;
-    const int64_t n = static_cast<int64_t>(p.a.total_q) * per_row;
+  if (blockIdx.x >= p.units) {  // queries: a warp per row and run of heads
+    constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes per head (two vectors each), heads per step
     const int lane = threadIdx.x & 31;
-    for (int64_t e0 = (blockIdx.x - p.units) * kAppendThreads + (threadIdx.x - lane); e0 < n;
-         e0 += static_cast<int64_t>(gridDim.x - p.units) * kAppendThreads) {
-      const int64_t e = min(e0 + lane, n - 1);
-      const int row = static_cast<int>(e / per_row), in = static_cast<int>(e % per_row);
-      const int b = paged_seq(p.a, row);
-      const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - __ldg(p.a.cu_q + b);
-      const bool ok = e0 + lane < n && (!p.half || (pos >= 0 && pos < p.n_pos));
-      float f[8];
-      if (ok) rotated8(p.q + row * p.q_stride + (in / kVecs) * D, (in % kVecs) * 8, static_cast<int>(pos), p, f);
-      __syncwarp();  // q_out may be q: a head's columns are all read before any is written
-      if (ok)
-        *reinterpret_cast<uint4*>(p.q_out + (static_cast<int64_t>(row) * p.n_h + in / kVecs) * D + (in % kVecs) * 8) =
-            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    const int64_t w = (blockIdx.x - p.units) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int64_t row = w / p.q_runs;
+    if (row >= p.a.total_q) return;
+    const int b = paged_seq(p.a, static_cast<int>(row));
+    const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - __ldg(p.a.cu_q + b);
+    if (p.half && (pos < 0 || pos >= p.n_pos)) return;
+    // the lane's two vectors: a rotating pair, or two neighbours behind the
+    // rotated columns; the angles are read once for all heads
+    const int i = lane % kLanes;
+    const bool turn = 8 * i < p.half;
+    const int c0 = !turn ? 16 * i : (p.interleaved ? 16 * i : 8 * i);
+    const int c1 = turn && !p.interleaved ? c0 + p.half : c0 + 8;
+    float cc[8], ss[8];
+    if (turn) {
+      const int64_t at = pos * p.half + 8 * i;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p.cos + at) + v), y = __ldg(reinterpret_cast<const float4*>(p.sin + at) + v);
+        cc[4 * v] = x.x; cc[4 * v + 1] = x.y; cc[4 * v + 2] = x.z; cc[4 * v + 3] = x.w;
+        ss[4 * v] = y.x; ss[4 * v + 1] = y.y; ss[4 * v + 2] = y.z; ss[4 * v + 3] = y.w;
+      }
+    }
+    const int h_end = min(p.n_h, static_cast<int>(w % p.q_runs + 1) * p.q_heads);
+#pragma unroll 4
+    for (int h = static_cast<int>(w % p.q_runs) * p.q_heads + lane / kLanes; h < h_end; h += kHeads) {
+      const dsa_bf16* x = p.q + row * p.q_stride + h * D;
+      uint4 u0 = *reinterpret_cast<const uint4*>(x + c0), u1 = *reinterpret_cast<const uint4*>(x + c1);
+      if (turn) {
+        float f[16];
+        bf16x8_to_f32(u0, *reinterpret_cast<float(*)[8]>(f));
+        bf16x8_to_f32(u1, *reinterpret_cast<float(*)[8]>(f + 8));
+        float g[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float ua = p.interleaved ? f[2 * e] : f[e], ub = p.interleaved ? f[2 * e + 1] : f[e + 8];
+          const float ra = __fsub_rn(__fmul_rn(ua, cc[e]), __fmul_rn(ub, ss[e]));
+          const float rb = __fadd_rn(__fmul_rn(ub, cc[e]), __fmul_rn(ua, ss[e]));
+          g[e] = ra;
+          g[e + 8] = rb;
+        }
+        if (p.interleaved) {
+          u0 = make_uint4(pack_bf16(g[0], g[8]), pack_bf16(g[1], g[9]), pack_bf16(g[2], g[10]), pack_bf16(g[3], g[11]));
+          u1 = make_uint4(pack_bf16(g[4], g[12]), pack_bf16(g[5], g[13]), pack_bf16(g[6], g[14]), pack_bf16(g[7], g[15]));
+        } else {
+          u0 = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
+          u1 = make_uint4(pack_bf16(g[8], g[9]), pack_bf16(g[10], g[11]), pack_bf16(g[12], g[13]), pack_bf16(g[14], g[15]));
+        }
+      }
+      dsa_bf16* y = p.q_out + (row * p.n_h + h) * D;
+      *reinterpret_cast<uint4*>(y + c0) = u0;
+      *reinterpret_cast<uint4*>(y + c1) = u1;
     }
     return;
   }
@@ -328,100 +366,188 @@ struct SelParams {
   PagedArgs a;
   const dsa_bf16* q;
   int n_h, page, inclusive, n_sel, n_first, n_last;
+  int ranks;                   // blocks of a decode row's cluster
+  int row_blocks, key_stride;  // many rows: blocks of a sequence, keys of a row
   int32_t* sel;
 };
 
-// One block per (row, head): pooled query codes, one score key per visible
-// page in shared memory, an 8-bit radix select of the n_sel-th largest key
-// and an ordered scan that writes the pages above it (ties: lowest first).
+// 8-bit codes of the pooled query of a row and head (the exact sum over the
+// group, rounded once); one warp, D / 32 columns per lane.
+template <int D>
+__device__ __forceinline__ void pooled_query(const SelParams& p, int64_t row, int head, int8_t* qc) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x & 31, G = p.n_h / p.a.n_kv;
+  const dsa_bf16* x = p.q + (row * p.n_h + head * G) * D + lane * kCols;
+  double acc[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) acc[i] = 0.0;
+#pragma unroll 4
+  for (int h = 0; h < G; ++h)
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(x + h * D) + i);
+      acc[2 * i] += static_cast<double>(__uint_as_float(w << 16));
+      acc[2 * i + 1] += static_cast<double>(__uint_as_float(w & 0xffff0000u));
+    }
+  float f[kCols], amax = 0.f;
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) {
+    f[i] = static_cast<float>(acc[i]);
+    fine = fine && fabsf(f[i]) <= kMaxF32;
+    amax = fmaxf(amax, fabsf(f[i]));
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  fine = __all_sync(0xffffffffu, fine) && amax >= kMinTop;
+  const float inv = __fmul_rn(127.f, __frcp_rn(amax));
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) qc[lane * kCols + i] = fine ? static_cast<int8_t>(__float2int_rn(__fmul_rn(f[i], inv))) : 0;
+}
+
+template <int D>
+__device__ __forceinline__ int dot_codes(const int4 (&s)[D / 16], const int8_t* qc) {
+  int dot = 0;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const int4 x = *reinterpret_cast<const int4*>(qc + 16 * i);
+    dot = __dp4a(s[i].x, x.x, __dp4a(s[i].y, x.y, __dp4a(s[i].z, x.z, __dp4a(s[i].w, x.w, dot))));
+  }
+  return dot;
+}
+template <int D>
+__device__ __forceinline__ void load_summary(const PagedArgs& a, int64_t unit, int4 (&s)[D / 16], float& scale) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) s[i] = __ldg(reinterpret_cast<const int4*>(a.sum + unit * D) + i);
+  scale = __ldg(a.sum_scale + unit);
+}
+
+// A key halfway between lo and hi: first by value (float keys crowd around
+// zero), later by key, so that the search ends whatever the values are.
+__device__ __forceinline__ uint32_t key_between(uint32_t lo, uint32_t hi, int step) {
+  uint32_t mid = lo + (hi - lo) / 2;
+  if (step < 14 && hi < 0xff800000u && lo > 0x007fffffu) {
+    const auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
+    const uint32_t m = float_key(0.5f * value(lo) + 0.5f * value(hi));
+    if (m > lo && m < hi) mid = m;
+  }
+  return mid;
+}
+
+constexpr uint32_t kForced = 0xffffffffu;  // above the key of every finite score
+
+// Decode rows: one cluster per (row, head).  Each block scores a part of the
+// row's pages and puts the keys into the first block's shared memory, which
+// then searches the n_sel-th largest key by halving (a count per step, one
+// block barrier each, the keys in registers) and writes the pages in order.
+// Bound by the summaries' bytes and, for few pages, by the chain of latencies.
+constexpr int kSelRegs = 16;  // keys per thread held in registers: 4,096 pages
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int8_t qc[D];
-  __shared__ float red[kSelThreads / 32];
-  __shared__ int hist[256], scan[kSelThreads / 32], pick[2];
+  __shared__ int counts[2][kSelThreads / 32], scan[kSelThreads / 32];
+  __shared__ uint32_t red[2][kSelThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;
   pdl_trigger();
   pdl_wait();
-  const int row = blockIdx.x / p.a.n_kv, head = blockIdx.x % p.a.n_kv;
+  const int64_t u = blockIdx.x / ranks;
+  const int row = static_cast<int>(u / p.a.n_kv), head = static_cast<int>(u % p.a.n_kv);
   const int b = paged_seq(p.a, row);
   const int t = paged_visible(p.a, b, row - __ldg(p.a.cu_q + b), p.inclusive);
   const int n = (t + p.page - 1) / p.page;
-  int32_t* out = p.sel + (static_cast<int64_t>(row) * p.a.n_kv + head) * p.n_sel;
-  if (n <= p.n_sel) {
-    for (int e = tid; e < p.n_sel; e += kSelThreads) out[e] = e < n ? e : -1;
+  int32_t* out = p.sel + u * p.n_sel;
+  if (n <= p.n_sel) {  // the same for the whole cluster
+    if (rank == 0)
+      for (int e = tid; e < p.n_sel; e += kSelThreads) out[e] = e < n ? e : -1;
     return;
   }
-  // pooled query: the exact sum over the group, rounded once
-  const int G = p.n_h / p.a.n_kv;
-  float qs = 0.f;
-  if (tid < D) {
-    const dsa_bf16* x = p.q + (static_cast<int64_t>(row) * p.n_h + head * G) * D + tid;
-    double acc = 0.0;
-    for (int h = 0; h < G; ++h) acc += static_cast<double>(__uint_as_float(static_cast<uint32_t>(__ldg(x + h * D)) << 16));
-    qs = static_cast<float>(acc);
-  }
-  const bool fine = __syncthreads_and(fabsf(qs) <= kMaxF32);
-  const float amax = block_max(fabsf(qs), red);
-  if (tid < D) qc[tid] = fine && amax >= kMinTop ? static_cast<int8_t>(__float2int_rn(__fmul_rn(qs, __fmul_rn(127.f, __frcp_rn(amax))))) : 0;
+  if (warp == 0) pooled_query<D>(p, row, head, qc);
   __syncthreads();
-  for (int j = tid; j < n; j += kSelThreads) {
-    uint32_t key = 0xffffffffu;
+  if (ranks > 1) cluster_sync();  // the first block runs before its memory is written
+  const int part = (n + ranks - 1) / ranks, j1 = min(n, (rank + 1) * part);
+  const uint32_t dst = mapa_shared(smem_u32(keys), 0);
+  for (int j = rank * part + tid; j < j1; j += kSelThreads) {
+    uint32_t key = kForced;
     if (j >= p.n_first && j < n - p.n_last) {
       const int pg = paged_page(p.a, b, j);
       key = 0u;
       if (pg >= 0) {
-        const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
-        const int4* s4 = reinterpret_cast<const int4*>(p.a.sum + unit * D);
-        int dot = 0;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int4 w = __ldg(s4 + i);
-          const int4 x = *reinterpret_cast<const int4*>(qc + 16 * i);
-          dot = __dp4a(w.x, x.x, __dp4a(w.y, x.y, __dp4a(w.z, x.z, __dp4a(w.w, x.w, dot))));
-        }
-        key = float_key(__fmul_rn(static_cast<float>(dot), __ldg(p.a.sum_scale + unit)));
+        int4 s[D / 16];
+        float scale;
+        load_summary<D>(p.a, static_cast<int64_t>(pg) * p.a.n_kv + head, s, scale);
+        key = float_key(__fmul_rn(static_cast<float>(dot_codes<D>(s, qc)), scale));
       }
     }
-    keys[j] = key;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
+  }
+  if (ranks > 1) {
+    cluster_sync();
+    if (rank) return;
+  } else {
+    __syncthreads();
   }
   // ---- the n_sel-th largest key
-  uint32_t prefix = 0;
-  int want = p.n_sel;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < n; j += kSelThreads)
-      if (shift == 24 || (keys[j] >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
-    __syncthreads();
-    if (warp == 0) {  // bins from the top, 8 per lane
-      int s = 0;
+  uint32_t k[kSelRegs];
+  const bool in_regs = n <= kSelRegs * kSelThreads;
+  uint32_t low = kForced, high = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += hist[255 - (lane * 8 + i)];
-      int incl = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      int above = incl - s;
-      if (above < want && incl >= want) {
-        int i = 0;
-        for (; above + hist[255 - (lane * 8 + i)] < want; ++i) above += hist[255 - (lane * 8 + i)];
-        pick[0] = 255 - (lane * 8 + i);
-        pick[1] = want - above;
-      }
-    }
-    __syncthreads();
-    prefix |= static_cast<uint32_t>(pick[0]) << shift;
-    want = pick[1];
+  for (int i = 0; i < kSelRegs; ++i) {
+    const int j = i * kSelThreads + tid;
+    k[i] = j < n ? keys[j] : 0u;
   }
-  // ---- ordered output: keys above the threshold, and the first `want` equal to it
+  for (int j = tid; j < n; j += kSelThreads) {
+    const uint32_t x = keys[j];
+    low = min(low, x);
+    if (x != kForced) high = max(high, x);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) { red[0][warp] = low; red[1][warp] = high; }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) { low = min(low, red[0][w]); high = max(high, red[1][w]); }
+  uint32_t hi = high + 1u;  // fewer than n_sel keys are >= hi, at least n_sel are >= low
+  int above = 0, step = 0;
+  const auto count = [&](uint32_t mid) {
+    int c = 0;
+    if (in_regs) {
+#pragma unroll
+      for (int i = 0; i < kSelRegs; ++i) c += k[i] >= mid;
+    } else {
+      for (int j = tid; j < n; j += kSelThreads) c += keys[j] >= mid;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) counts[step & 1][warp] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) c += counts[step & 1][w];
+    return c;
+  };
+  bool exact = false;
+  above = p.n_first + p.n_last;
+  if (above >= p.n_sel) { low = kForced; exact = true; }  // the forced pages alone
+  while (!exact && hi - low > 1u) {
+    const uint32_t mid = key_between(low, hi, step);
+    const int c = count(mid);
+    ++step;
+    if (c >= p.n_sel) {
+      low = mid;
+      exact = c == p.n_sel;
+    } else {
+      hi = mid;
+      above = c;
+    }
+  }
+  const int want = exact ? p.n_sel : p.n_sel - above;  // keys equal to low that are taken
+  // ---- ordered output: keys above low, and the first `want` equal to it
   int at = 0, ties = 0;
   for (int j0 = 0; j0 < n; j0 += kSelThreads) {
     const int j = j0 + tid;
     const uint32_t key = j < n ? keys[j] : 0u;
-    const bool gt = j < n && key > prefix, eq = j < n && key == prefix;
+    const bool gt = j < n && (exact ? key >= low : key > low), eq = j < n && !exact && key == low;
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     __syncthreads();
     if (lane == 0) scan[warp] = __popc(bg) | (__popc(be) << 16);
@@ -441,6 +567,110 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
     else if (eq && e0 < want) out[g0 + e0] = j;
     at += gsum;
     ties += esum;
+  }
+}
+
+// Many rows: one block per (eight rows of a sequence, head).  A page's summary
+// is read once for the eight rows; then a warp selects for each row, its keys
+// in registers (up to 1,024 pages) or in shared memory.
+constexpr int kSelRows = 8;
+template <int D>
+__global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelParams p) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [kSelRows][p.key_stride]
+  __shared__ __align__(16) int8_t qc[kSelRows][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int head = blockIdx.x % p.a.n_kv;
+  const int rest = blockIdx.x / p.a.n_kv;
+  const int b = rest / p.row_blocks;
+  int r0, rows;
+  paged_rows(p.a, b, r0, rows);
+  const int first = rest % p.row_blocks * kSelRows;
+  const int nr = min(kSelRows, rows - first);
+  if (nr <= 0) return;
+  const auto pages_of = [&](int r) { return (paged_visible(p.a, b, first + r, p.inclusive) + p.page - 1) / p.page; };
+  const int n_max = pages_of(nr - 1);
+  const int n = warp < nr ? pages_of(warp) : 0;
+  if (n_max > p.n_sel) {
+    if (warp < nr) pooled_query<D>(p, r0 + first + warp, head, qc[warp]);
+    __syncthreads();
+    const int tail = p.page, t0 = paged_visible(p.a, b, first, p.inclusive);
+#pragma unroll 2
+    for (int j = tid; j < n_max; j += kSelThreads) {
+      const int pg = paged_page(p.a, b, j);
+      int4 s[D / 16];
+      float scale = 0.f;
+      if (pg >= 0) load_summary<D>(p.a, static_cast<int64_t>(pg) * p.a.n_kv + head, s, scale);
+      for (int r = 0; r < nr; ++r) {
+        const int nn = (min(t0 + r, p.a.max_Lk) + tail - 1) / tail;
+        uint32_t key = kForced;
+        if (j >= p.n_first && j < nn - p.n_last) key = pg >= 0 ? float_key(__fmul_rn(static_cast<float>(dot_codes<D>(s, qc[r])), scale)) : 0u;
+        keys[r * p.key_stride + j] = key;
+      }
+    }
+    __syncthreads();
+  }
+  if (warp >= nr) return;
+  int32_t* out = p.sel + ((static_cast<int64_t>(r0) + first + warp) * p.a.n_kv + head) * p.n_sel;
+  if (n <= p.n_sel) {
+    for (int e = lane; e < p.n_sel; e += 32) out[e] = e < n ? e : -1;
+    return;
+  }
+  const uint32_t* kr = keys + warp * p.key_stride;
+  constexpr int kRegs = 32;
+  const bool in_regs = n <= 32 * kRegs;
+  uint32_t k[kRegs];
+  uint32_t low = kForced, hi = 0u;
+  if (in_regs) {
+#pragma unroll
+    for (int i = 0; i < kRegs; ++i) {
+      k[i] = i * 32 + lane < n ? kr[i * 32 + lane] : 0u;
+      if (i * 32 + lane < n) low = min(low, k[i]);
+      if (k[i] != kForced) hi = max(hi, k[i]);
+    }
+  } else {
+    for (int j = lane; j < n; j += 32) {
+      low = min(low, kr[j]);
+      if (kr[j] != kForced) hi = max(hi, kr[j]);
+    }
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
+  int above = p.n_first + p.n_last;
+  bool exact = false;
+  if (above >= p.n_sel) { low = kForced; exact = true; }
+  for (int step = 0; !exact && hi - low > 1u; ++step) {
+    const uint32_t mid = key_between(low, hi, step);
+    int c = 0;
+    if (in_regs) {
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i) c += k[i] >= mid;
+    } else {
+      for (int j = lane; j < n; j += 32) c += kr[j] >= mid;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= p.n_sel) {
+      low = mid;
+      exact = c == p.n_sel;
+    } else {
+      hi = mid;
+      above = c;
+    }
+  }
+  const int want = exact ? p.n_sel : p.n_sel - above;
+  int at = 0, ties = 0;
+  const unsigned lt = (1u << lane) - 1u;
+  for (int j0 = 0; j0 < n && at + min(ties, want) < p.n_sel; j0 += 32) {
+    const int j = j0 + lane;
+    const uint32_t key = j < n ? kr[j] : 0u;
+    const bool gt = j < n && (exact ? key >= low : key > low), eq = j < n && !exact && key == low;
+    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
+    if (gt) out[g0 + min(e0, want)] = j;
+    else if (eq && e0 < want) out[g0 + e0] = j;
+    at += __popc(bg);
+    ties += __popc(be);
   }
 }
 
@@ -478,8 +708,15 @@ dsa_status dsa_paged_append(const dsa_paged_kv* kv, const dsa_paged_batch* batch
   p.cos = cos; p.sin = sin; p.n_h = n_h; p.half = rot / 2; p.interleaved = interleaved; p.n_pos = n_pos;
   p.touched = (batch->max_Lq + kv->page - 2) / kv->page + 1;
   p.units = 2ll * batch->B * p.touched * kv->n_kv;
-  const int64_t q_blocks = q ? (static_cast<int64_t>(batch->total_q) * n_h * (kv->D / 8) + kAppendThreads - 1) / kAppendThreads : 0;
-  const int64_t grid = p.units + std::min<int64_t>(q_blocks, 1 << 20);
+  // queries: long runs of heads reuse a row's angles; few rows are cut into
+  // short runs so that some 2,000 warps share the work
+  const int step = 512 / kv->D;  // heads of a warp's step
+  const int steps = q ? (n_h + step - 1) / step : 1;
+  const int per = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, static_cast<int64_t>(batch->total_q) * steps / 2048)));
+  p.q_heads = per * step;
+  p.q_runs = q ? (n_h + p.q_heads - 1) / p.q_heads : 1;
+  const int64_t q_blocks = q ? (static_cast<int64_t>(batch->total_q) * p.q_runs + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : 0;
+  const int64_t grid = p.units + q_blocks;
   if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: batch too large");
   const cudaError_t e = kv->D == 64
       ? launch_append<64>(p, kv->page, kv->fmt == DSA_KV_E4M3, static_cast<unsigned>(grid), static_cast<cudaStream_t>(stream))
@@ -503,16 +740,46 @@ dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, con
   const int max_n = (batch->max_Lk + kv->page - 1) / kv->page;
   if (n_sel > 1024 || max_n > kSelMaxPages)
     return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: n_sel <= 1024 and at most 49152 pages per sequence");
-  const int64_t grid = static_cast<int64_t>(batch->total_q) * kv->n_kv;
-  if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
   p.q = q; p.n_h = n_h; p.page = kv->page; p.inclusive = inclusive; p.n_sel = n_sel; p.n_first = n_first; p.n_last = n_last;
   p.sel = sel;
-  const int smem = max_n * 4;
-  const void* fn = kv->D == 64 ? reinterpret_cast<const void*>(page_topk_kernel<64>) : reinterpret_cast<const void*>(page_topk_kernel<128>);
-  cudaError_t e = ensure_smem_limit(fn, smem);
-  if (e == cudaSuccess)
-    e = launch_pdl(kv->D == 64 ? page_topk_kernel<64> : page_topk_kernel<128>, dim3(static_cast<unsigned>(grid)), dim3(kSelThreads),
-                   smem, static_cast<cudaStream_t>(stream), p);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool d64 = kv->D == 64;
+  // Eight rows share a block when sequences have that many rows and the keys
+  // of eight rows fit in shared memory; otherwise each row has a cluster.
+  p.key_stride = (max_n + 3) / 4 * 4;
+  cudaError_t e;
+  if (batch->max_Lq >= 4 && kSelRows * p.key_stride * 4 <= 200 * 1024) {
+    p.row_blocks = (batch->max_Lq + kSelRows - 1) / kSelRows;
+    const int64_t grid = static_cast<int64_t>(batch->B) * p.row_blocks * kv->n_kv;
+    if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
+    auto fn = d64 ? page_topk_rows_kernel<64> : page_topk_rows_kernel<128>;
+    const int smem = kSelRows * p.key_stride * 4;
+    e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem);
+    if (e == cudaSuccess) e = launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kSelThreads), smem, s, p);
+  } else {
+    const int64_t units = static_cast<int64_t>(batch->total_q) * kv->n_kv;
+    // a block scores 256 pages at a time; about four blocks per SM in all
+    p.ranks = 1;
+    while (p.ranks < 8 && max_n > 256 * p.ranks && units * p.ranks < 300) p.ranks *= 2;
+    if (units * p.ranks > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
+    auto fn = d64 ? page_topk_kernel<64> : page_topk_kernel<128>;
+    const int smem = p.key_stride * 4;
+    e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(units * p.ranks));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.ranks);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, fn, p);
+  }
   if (e != cudaSuccess) return set_error(DSA_ERR_CUDA, std::string("dsa_page_topk launch: ") + cudaGetErrorString(e));
   return DSA_OK;
 }
