@@ -446,7 +446,7 @@ template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int8_t qc[D];
-  __shared__ int counts[2][kSelThreads / 32], scan[kSelThreads / 32];
+  __shared__ int counts[2][kSelThreads / 32], scan[2][kSelThreads / 32];
   __shared__ uint32_t red[2][kSelThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;
@@ -468,19 +468,26 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   if (ranks > 1) cluster_sync();  // the first block runs before its memory is written
   const int part = (n + ranks - 1) / ranks, j1 = min(n, (rank + 1) * part);
   const uint32_t dst = mapa_shared(smem_u32(keys), 0);
-  for (int j = rank * part + tid; j < j1; j += kSelThreads) {
-    uint32_t key = kForced;
-    if (j >= p.n_first && j < n - p.n_last) {
-      const int pg = paged_page(p.a, b, j);
-      key = 0u;
-      if (pg >= 0) {
-        int4 s[D / 16];
-        float scale;
-        load_summary<D>(p.a, static_cast<int64_t>(pg) * p.a.n_kv + head, s, scale);
-        key = float_key(__fmul_rn(static_cast<float>(dot_codes<D>(s, qc)), scale));
-      }
+  // D / 16 lanes per page, 16 bytes each: whole lines, and the dot over lanes
+  constexpr int kLanes = D / 16, kPages = 32 / kLanes;
+  const int4 mine = *reinterpret_cast<const int4*>(qc + lane % kLanes * 16);
+#pragma unroll 4
+  for (int j0 = rank * part + warp * kPages; j0 < j1; j0 += kSelThreads / kLanes) {
+    const int j = j0 + lane / kLanes;
+    const bool scored = j < j1 && j >= p.n_first && j < n - p.n_last;
+    const int pg = scored ? paged_page(p.a, b, j) : -1;
+    int4 w = make_int4(0, 0, 0, 0);
+    float scale = 0.f;
+    if (pg >= 0) {
+      const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
+      w = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D) + lane % kLanes);
+      scale = __ldg(p.a.sum_scale + unit);
     }
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
+    int dot = __dp4a(w.x, mine.x, __dp4a(w.y, mine.y, __dp4a(w.z, mine.z, __dp4a(w.w, mine.w, 0))));
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    const uint32_t key = !scored ? kForced : (pg >= 0 ? float_key(__fmul_rn(static_cast<float>(dot), scale)) : 0u);
+    if (j < j1 && lane % kLanes == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
   }
   if (ranks > 1) {
     cluster_sync();
@@ -489,16 +496,15 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
     __syncthreads();
   }
   // ---- the n_sel-th largest key
+  // each warp owns a run of 32 * per pages
+  const int per = (n + kSelThreads - 1) / kSelThreads, w0 = warp * per * 32 + lane;
+  const bool in_regs = per <= kSelRegs;
   uint32_t k[kSelRegs];
-  const bool in_regs = n <= kSelRegs * kSelThreads;
   uint32_t low = kForced, high = 0u;
 #pragma unroll
-  for (int i = 0; i < kSelRegs; ++i) {
-    const int j = i * kSelThreads + tid;
-    k[i] = j < n ? keys[j] : 0u;
-  }
-  for (int j = tid; j < n; j += kSelThreads) {
-    const uint32_t x = keys[j];
+  for (int i = 0; i < kSelRegs; ++i) k[i] = i < per && w0 + i * 32 < n ? keys[w0 + i * 32] : 0u;
+  for (int i = 0; i < per; ++i) {
+    const uint32_t x = w0 + i * 32 < n ? keys[w0 + i * 32] : kForced;
     low = min(low, x);
     if (x != kForced) high = max(high, x);
   }
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
 #pragma unroll
       for (int i = 0; i < kSelRegs; ++i) c += k[i] >= mid;
     } else {
-      for (int j = tid; j < n; j += kSelThreads) c += keys[j] >= mid;
+      for (int i = 0; i < per; ++i) c += w0 + i * 32 < n && keys[w0 + i * 32] >= mid;
     }
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) counts[step & 1][warp] = c;
@@ -543,30 +549,35 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   }
   const int want = exact ? p.n_sel : p.n_sel - above;  // keys equal to low that are taken
   // ---- ordered output: keys above low, and the first `want` equal to it
+  // the warps count theirs, then write
+  const auto is_gt = [&](int i, uint32_t& key, bool& eq) {
+    const int j = w0 + i * 32;
+    key = j < n ? keys[j] : 0u;
+    eq = j < n && !exact && key == low;
+    return j < n && (exact ? key >= low : key > low);
+  };
   int at = 0, ties = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < n ? keys[j] : 0u;
-    const bool gt = j < n && (exact ? key >= low : key > low), eq = j < n && !exact && key == low;
+  for (int i = 0; i < per; ++i) {
+    uint32_t key;
+    bool eq;
+    at += __popc(__ballot_sync(0xffffffffu, is_gt(i, key, eq)));
+    ties += __popc(__ballot_sync(0xffffffffu, eq));
+  }
+  if (lane == 0) { scan[0][warp] = at; scan[1][warp] = ties; }
+  __syncthreads();
+  at = ties = 0;
+  for (int w = 0; w < warp; ++w) { at += scan[0][w]; ties += scan[1][w]; }
+  const unsigned lt = (1u << lane) - 1u;
+  for (int i = 0; i < per; ++i) {
+    uint32_t key;
+    bool eq;
+    const bool gt = is_gt(i, key, eq);
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) scan[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();
-    int g0 = at, e0 = ties, gsum = 0, esum = 0;
-#pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      const int c = scan[w];
-      if (w < warp) { g0 += c & 0xffff; e0 += c >> 16; }
-      gsum += c & 0xffff;
-      esum += c >> 16;
-    }
-    const unsigned lt = (1u << lane) - 1u;
-    g0 += __popc(bg & lt);
-    e0 += __popc(be & lt);
-    if (gt) out[g0 + min(e0, want)] = j;
-    else if (eq && e0 < want) out[g0 + e0] = j;
-    at += gsum;
-    ties += esum;
+    const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
+    if (gt) out[g0 + min(e0, want)] = w0 + i * 32;
+    else if (eq && e0 < want) out[g0 + e0] = w0 + i * 32;
+    at += __popc(bg);
+    ties += __popc(be);
   }
 }
 
