@@ -37,7 +37,8 @@ dsa_status check_paged_host(const char* who, const dsa_paged_kv* kv, const dsa_p
     return bad(DSA_ERR_INVALID_ARG, "the block table does not cover max_Lk positions");
   if (out)
     *out = PagedArgs{kv->k, kv->v, kv->k_scale, kv->v_scale, kv->sum, kv->sum_scale, kv->n_pages, kv->n_kv,
-                     pb->cu_q, pb->start_pos, pb->block_table, pb->B, pb->max_pages, pb->total_q, pb->max_Lq, pb->max_Lk};
+                     pb->cu_q, pb->start_pos, pb->block_table, pb->B, pb->max_pages, pb->total_q, pb->max_Lq, pb->max_Lk,
+                     pb->max_Lq == 1 && pb->total_q == pb->B};
   return DSA_OK;
 }
 
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     const int64_t row = w / p.q_runs;
     if (row >= p.a.total_q) return;
     const int b = paged_seq(p.a, static_cast<int>(row));
-    const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - __ldg(p.a.cu_q + b);
+    const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - paged_first(p.a, b);
     if (p.half && (pos < 0 || pos >= p.n_pos)) return;
     // the lane's two vectors: a rotating pair, or two neighbours behind the
     // rotated columns; the angles are read once for all heads
@@ -422,13 +423,14 @@ __device__ __forceinline__ void load_summary(const PagedArgs& a, int64_t unit, i
   scale = __ldg(a.sum_scale + unit);
 }
 
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+
 // A key halfway between lo and hi: first by value (float keys crowd around
 // zero), later by key, so that the search ends whatever the values are.
 __device__ __forceinline__ uint32_t key_between(uint32_t lo, uint32_t hi, int step) {
   uint32_t mid = lo + (hi - lo) / 2;
   if (step < 14 && hi < 0xff800000u && lo > 0x007fffffu) {
-    const auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
-    const uint32_t m = float_key(0.5f * value(lo) + 0.5f * value(hi));
+    const uint32_t m = float_key(0.5f * key_value(lo) + 0.5f * key_value(hi));
     if (m > lo && m < hi) mid = m;
   }
   return mid;
@@ -438,16 +440,19 @@ constexpr uint32_t kForced = 0xffffffffu;  // above the key of every finite scor
 
 // Decode rows: one cluster per (row, head).  Each block scores a part of the
 // row's pages and puts the keys into the first block's shared memory, which
-// then searches the n_sel-th largest key by halving (a count per step, one
-// block barrier each, the keys in registers) and writes the pages in order.
-// Bound by the summaries' bytes and, for few pages, by the chain of latencies.
-constexpr int kSelRegs = 16;  // keys per thread held in registers: 4,096 pages
+// finds the n_sel-th largest key and writes the pages in order: a histogram of
+// 1,024 equal steps of value, the keys of one step ranked against each other;
+// or halving, where a step holds too many keys.  Bound by the chain of
+// latencies (dependent loads, barriers): the work is split until the blocks
+// fill the GPU.
+constexpr int kDecThreads = 512, kDecWarps = kDecThreads / 32;
+constexpr int kBins = 1024, kRankMax = 256;
 template <int D>
-__global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams p) {
+__global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(16) int8_t qc[D];
-  __shared__ int counts[2][kSelThreads / 32], scan[2][kSelThreads / 32];
-  __shared__ uint32_t red[2][kSelThreads / 32];
+  __shared__ int hist[kBins], counts[2][kDecWarps], scan[2][kDecWarps], pick[4];
+  __shared__ uint32_t red[2][kDecWarps], cand[kRankMax];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank()), ranks = p.ranks;
   pdl_trigger();
@@ -455,39 +460,56 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   const int64_t u = blockIdx.x / ranks;
   const int row = static_cast<int>(u / p.a.n_kv), head = static_cast<int>(u % p.a.n_kv);
   const int b = paged_seq(p.a, row);
-  const int t = paged_visible(p.a, b, row - __ldg(p.a.cu_q + b), p.inclusive);
+  const int t = paged_visible(p.a, b, row - paged_first(p.a, b), p.inclusive);
   const int n = (t + p.page - 1) / p.page;
   int32_t* out = p.sel + u * p.n_sel;
   if (n <= p.n_sel) {  // the same for the whole cluster
     if (rank == 0)
-      for (int e = tid; e < p.n_sel; e += kSelThreads) out[e] = e < n ? e : -1;
+      for (int e = tid; e < p.n_sel; e += kDecThreads) out[e] = e < n ? e : -1;
     return;
   }
-  if (warp == 0) pooled_query<D>(p, row, head, qc);
-  __syncthreads();
-  if (ranks > 1) cluster_sync();  // the first block runs before its memory is written
+  // D / 16 lanes per page, 16 bytes each: whole lines, and the dot over lanes.
+  // The loads of a batch of pages are in flight before the first is used.
+  constexpr int kLanes = D / 16, kPages = 32 / kLanes, kStep = kDecThreads / kLanes, kBatch = 4;
   const int part = (n + ranks - 1) / ranks, j1 = min(n, (rank + 1) * part);
   const uint32_t dst = mapa_shared(smem_u32(keys), 0);
-  // D / 16 lanes per page, 16 bytes each: whole lines, and the dot over lanes
-  constexpr int kLanes = D / 16, kPages = 32 / kLanes;
-  const int4 mine = *reinterpret_cast<const int4*>(qc + lane % kLanes * 16);
-#pragma unroll 4
-  for (int j0 = rank * part + warp * kPages; j0 < j1; j0 += kSelThreads / kLanes) {
-    const int j = j0 + lane / kLanes;
-    const bool scored = j < j1 && j >= p.n_first && j < n - p.n_last;
-    const int pg = scored ? paged_page(p.a, b, j) : -1;
-    int4 w = make_int4(0, 0, 0, 0);
-    float scale = 0.f;
-    if (pg >= 0) {
-      const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
-      w = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D) + lane % kLanes);
-      scale = __ldg(p.a.sum_scale + unit);
-    }
-    int dot = __dp4a(w.x, mine.x, __dp4a(w.y, mine.y, __dp4a(w.z, mine.z, __dp4a(w.w, mine.w, 0))));
+  int pg[kBatch];
+  const auto page_of = [&](int j) { return j < j1 && j >= p.n_first && j < n - p.n_last ? paged_page(p.a, b, j) : -1; };
+  const int first = rank * part + warp * kPages + lane / kLanes;
 #pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const uint32_t key = !scored ? kForced : (pg >= 0 ? float_key(__fmul_rn(static_cast<float>(dot), scale)) : 0u);
-    if (j < j1 && lane % kLanes == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
+  for (int e = 0; e < kBatch; ++e) pg[e] = page_of(first + e * kStep);
+  if (warp == 0) pooled_query<D>(p, row, head, qc);
+  if (rank == 0)
+    for (int i = tid; i < kBins; i += kDecThreads) hist[i] = 0;
+  if (ranks > 1) cluster_sync();  // the first block runs before its memory is written
+  else __syncthreads();
+  const int4 mine = *reinterpret_cast<const int4*>(qc + lane % kLanes * 16);
+  for (int j0 = first; j0 - lane / kLanes < j1; j0 += kBatch * kStep) {
+    int4 w[kBatch];
+    float scale[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      w[e] = make_int4(0, 0, 0, 0);
+      scale[e] = 0.f;
+      if (pg[e] >= 0) {
+        const int64_t unit = static_cast<int64_t>(pg[e]) * p.a.n_kv + head;
+        w[e] = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D) + lane % kLanes);
+        scale[e] = __ldg(p.a.sum_scale + unit);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) pg[e] = page_of(j0 + (kBatch + e) * kStep);
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int j = j0 + e * kStep;
+      int dot = __dp4a(w[e].x, mine.x, __dp4a(w[e].y, mine.y, __dp4a(w[e].z, mine.z, __dp4a(w[e].w, mine.w, 0))));
+#pragma unroll
+      for (int o = kLanes / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      const bool scored = j >= p.n_first && j < n - p.n_last;
+      // (a page outside the pool leaves the zeros: score 0)
+      const uint32_t key = scored ? float_key(__fmul_rn(static_cast<float>(dot), scale[e])) : kForced;
+      if (j < j1 && lane % kLanes == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
+    }
   }
   if (ranks > 1) {
     cluster_sync();
@@ -495,14 +517,9 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   } else {
     __syncthreads();
   }
-  // ---- the n_sel-th largest key
-  // each warp owns a run of 32 * per pages
-  const int per = (n + kSelThreads - 1) / kSelThreads, w0 = warp * per * 32 + lane;
-  const bool in_regs = per <= kSelRegs;
-  uint32_t k[kSelRegs];
+  // ---- the n_sel-th largest key.  Each warp owns a run of 32 * per pages.
+  const int per = (n + kDecThreads - 1) / kDecThreads, w0 = warp * per * 32 + lane;
   uint32_t low = kForced, high = 0u;
-#pragma unroll
-  for (int i = 0; i < kSelRegs; ++i) k[i] = i < per && w0 + i * 32 < n ? keys[w0 + i * 32] : 0u;
   for (int i = 0; i < per; ++i) {
     const uint32_t x = w0 + i * 32 < n ? keys[w0 + i * 32] : kForced;
     low = min(low, x);
@@ -511,34 +528,79 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
   if (lane == 0) { red[0][warp] = low; red[1][warp] = high; }
+  if (tid == 0) pick[0] = -1;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) { low = min(low, red[0][w]); high = max(high, red[1][w]); }
+  low = __reduce_min_sync(0xffffffffu, red[0][lane % kDecWarps]);
+  high = __reduce_max_sync(0xffffffffu, red[1][lane % kDecWarps]);
   uint32_t hi = high + 1u;  // fewer than n_sel keys are >= hi, at least n_sel are >= low
-  int above = 0, step = 0;
-  const auto count = [&](uint32_t mid) {
-    int c = 0;
-    if (in_regs) {
-#pragma unroll
-      for (int i = 0; i < kSelRegs; ++i) c += k[i] >= mid;
-    } else {
-      for (int i = 0; i < per; ++i) c += w0 + i * 32 < n && keys[w0 + i * 32] >= mid;
+  int above = p.n_first + p.n_last;
+  bool exact = above >= p.n_sel;  // exactly the keys >= low are taken
+  if (exact) low = kForced;       // the forced pages alone
+  const float v0 = key_value(low), gain = kBins / (key_value(high) - v0);
+  if (!exact && high > low && gain < 1e30f) {
+    const auto bin = [&](uint32_t key) { return min(kBins - 1, static_cast<int>((key_value(key) - v0) * gain)); };  // grows with the value
+    for (int i = 0; i < per; ++i) {
+      const uint32_t x = w0 + i * 32 < n ? keys[w0 + i * 32] : kForced;
+      if (x != kForced) atomicAdd(&hist[bin(x)], 1);
     }
+    __syncthreads();
+    if (warp == 0) {
+      int run = above;
+      for (int i = 0; i < kBins / 32; ++i) {  // 32 bins at a time, the highest in lane 0
+        const int c = hist[kBins - 1 - (i * 32 + lane)];
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, run + incl >= p.n_sel);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            pick[0] = kBins - 1 - (i * 32 + lane);
+            pick[1] = run + incl - c;  // keys above the bin
+            pick[2] = c;
+            pick[3] = 0;
+          }
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+    const int sel_bin = pick[0], in_bin = pick[2];
+    if (in_bin <= kRankMax) {  // rank the bin's keys against each other
+      for (int i = 0; i < per; ++i) {
+        const uint32_t x = w0 + i * 32 < n ? keys[w0 + i * 32] : kForced;
+        if (x != kForced && bin(x) == sel_bin) cand[atomicAdd(&pick[3], 1)] = x;  // any order
+      }
+      __syncthreads();
+      above = pick[1];
+      if (tid < in_bin) {
+        int gt = 0, ge = 0;
+        for (int i = 0; i < in_bin; ++i) { gt += cand[i] > cand[tid]; ge += cand[i] >= cand[tid]; }
+        if (above + gt < p.n_sel && above + ge >= p.n_sel) {  // equal candidates write the same
+          red[0][0] = cand[tid];
+          counts[0][0] = above + gt;
+          counts[0][1] = above + ge;
+        }
+      }
+      __syncthreads();
+      low = red[0][0];
+      above = counts[0][0];
+      exact = counts[0][1] == p.n_sel;
+      hi = low + 1u;
+    }
+  }
+  __syncthreads();
+  for (int step = 0; !exact && hi - low > 1u; ++step) {
+    const uint32_t mid = key_between(low, hi, step);
+    int c = 0;
+    for (int i = 0; i < per; ++i) c += w0 + i * 32 < n && keys[w0 + i * 32] >= mid;
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) counts[step & 1][warp] = c;
     __syncthreads();
-    c = 0;
-#pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) c += counts[step & 1][w];
-    return c;
-  };
-  bool exact = false;
-  above = p.n_first + p.n_last;
-  if (above >= p.n_sel) { low = kForced; exact = true; }  // the forced pages alone
-  while (!exact && hi - low > 1u) {
-    const uint32_t mid = key_between(low, hi, step);
-    const int c = count(mid);
-    ++step;
+    c = __reduce_add_sync(0xffffffffu, lane < kDecWarps ? counts[step & 1][lane] : 0);
     if (c >= p.n_sel) {
       low = mid;
       exact = c == p.n_sel;
@@ -548,30 +610,32 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_kernel(const SelParams 
     }
   }
   const int want = exact ? p.n_sel : p.n_sel - above;  // keys equal to low that are taken
-  // ---- ordered output: keys above low, and the first `want` equal to it
-  // the warps count theirs, then write
-  const auto is_gt = [&](int i, uint32_t& key, bool& eq) {
+  // ---- ordered output: keys above low, and the first `want` equal to it; the
+  // warps count theirs, then write
+  const auto is_gt = [&](int i, bool& eq) {
     const int j = w0 + i * 32;
-    key = j < n ? keys[j] : 0u;
+    const uint32_t key = j < n ? keys[j] : 0u;
     eq = j < n && !exact && key == low;
     return j < n && (exact ? key >= low : key > low);
   };
   int at = 0, ties = 0;
   for (int i = 0; i < per; ++i) {
-    uint32_t key;
     bool eq;
-    at += __popc(__ballot_sync(0xffffffffu, is_gt(i, key, eq)));
-    ties += __popc(__ballot_sync(0xffffffffu, eq));
+    at += is_gt(i, eq);
+    ties += eq;
   }
+  at = __reduce_add_sync(0xffffffffu, at);
+  ties = __reduce_add_sync(0xffffffffu, ties);
   if (lane == 0) { scan[0][warp] = at; scan[1][warp] = ties; }
+  const bool some = at + ties > 0;
   __syncthreads();
-  at = ties = 0;
-  for (int w = 0; w < warp; ++w) { at += scan[0][w]; ties += scan[1][w]; }
+  if (!some) return;
+  at = __reduce_add_sync(0xffffffffu, lane < warp ? scan[0][lane] : 0);
+  ties = __reduce_add_sync(0xffffffffu, lane < warp ? scan[1][lane] : 0);
   const unsigned lt = (1u << lane) - 1u;
   for (int i = 0; i < per; ++i) {
-    uint32_t key;
     bool eq;
-    const bool gt = is_gt(i, key, eq);
+    const bool gt = is_gt(i, eq);
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
     if (gt) out[g0 + min(e0, want)] = w0 + i * 32;
@@ -769,16 +833,18 @@ dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, con
     if (e == cudaSuccess) e = launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kSelThreads), smem, s, p);
   } else {
     const int64_t units = static_cast<int64_t>(batch->total_q) * kv->n_kv;
-    // a block scores 256 pages at a time; about four blocks per SM in all
+    // 256 pages and more per block, at most two blocks per SM in all (at 8
+    // sequences x 8 heads x 3,125 pages: 1, 2, 4, 8 blocks 23.5, 18.6, 14.8,
+    // 22.8 us; eight no longer fit at once)
     p.ranks = 1;
-    while (p.ranks < 8 && max_n > 256 * p.ranks && units * p.ranks < 300) p.ranks *= 2;
+    while (p.ranks < 8 && max_n > 256 * p.ranks && units * p.ranks * 2 <= 300) p.ranks *= 2;
     if (units * p.ranks > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
     auto fn = d64 ? page_topk_kernel<64> : page_topk_kernel<128>;
     const int smem = p.key_stride * 4;
     e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(units * p.ranks));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(kDecThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

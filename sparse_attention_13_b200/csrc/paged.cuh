@@ -18,17 +18,20 @@ struct PagedArgs {
   int n_pages, n_kv;
   const int *cu_q, *sp, *bt;
   int B, max_pages, total_q, max_Lq, max_Lk;
+  bool one;  // every sequence has one row (the contract then fixes cu_q: no loads for it)
 };
 
 // Row range of sequence b, clamped so that a batch that breaks its contract
 // still names only rows of the tensors.
 __device__ __forceinline__ void paged_rows(const PagedArgs& a, int b, int& r0, int& n) {
+  if (a.one) { r0 = b; n = 1; return; }
   r0 = min(max(__ldg(a.cu_q + b), 0), a.total_q);
   n = min(max(__ldg(a.cu_q + b + 1) - r0, 0), min(a.max_Lq, a.total_q - r0));
 }
 
 // Sequence of a packed row: the last b with cu_q[b] <= row.
 __device__ __forceinline__ int paged_seq(const PagedArgs& a, int row) {
+  if (a.one) return row;
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -36,6 +39,9 @@ __device__ __forceinline__ int paged_seq(const PagedArgs& a, int row) {
   }
   return lo;
 }
+
+// First packed row of sequence b.
+__device__ __forceinline__ int paged_first(const PagedArgs& a, int b) { return a.one ? b : __ldg(a.cu_q + b); }
 
 // Positions visible to the row: s < start_pos + i (+ 1 when inclusive).
 __device__ __forceinline__ int paged_visible(const PagedArgs& a, int b, int i, int inclusive) {

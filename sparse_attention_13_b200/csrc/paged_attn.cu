@@ -124,7 +124,7 @@ struct Walker {
       s.h0 = rem % p.hbs * p.Gx;
       s.b = paged_seq(p.a, s.row0);
       s.nr = 1;
-      s.t0 = s.t1 = paged_visible(p.a, s.b, s.row0 - __ldg(p.a.cu_q + s.b), p.inclusive);
+      s.t0 = s.t1 = paged_visible(p.a, s.b, s.row0 - paged_first(p.a, s.b), p.inclusive);
     } else {
       while (pos >= base + weight) {
         base += weight;

@@ -361,7 +361,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int tok = m / p.G, g = m - tok * p.G;
     const int row = q * p.tok + tok;               // row of the unit
     const bool live = tok < p.tok && row < u.rows;
-    const int t = live ? paged_visible(p.a, u.b, u.row0 - __ldg(p.a.cu_q + u.b) + row, p.inclusive) : 0;
+    const int t = live ? paged_visible(p.a, u.b, u.row0 - paged_first(p.a, u.b) + row, p.inclusive) : 0;
     const int64_t at = static_cast<int64_t>(u.row0 + row) * p.n_h + u.kvh * p.G + g;
     float cr = p.scale_log2;  // factor of the row's scores
     {
