@@ -25,7 +25,57 @@ constexpr int kSoftWarps = 8, kConvWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
 constexpr int kThreads = 16 * 32;  // four warpgroups, for the register split (two warps idle)
 // 65,536 registers: 128 a thread at launch; 2 x 128 x 208 + 2 x 128 x 48
 constexpr int kSoftRegs = 208, kOtherRegs = 48;
-constexpr float kLazy = 8.f;   // a row's reference exponent may lag its maximum by this much
+// A row's reference exponent may lag its maximum until sixteen weights sum to
+// more than this (f16 holds 2^16): rescaling O is rare, and no maximum is taken
+// on the way.
+constexpr float kMostSum = 4096.f;
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f32x2_parts(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Sixteen weights of a row: 2^(score * k + add), zero from column lim - col on
+// (EDGE), rounded and packed two to a word.  Returns their f32 sum.
+template <bool F8, bool EDGE>
+__device__ __forceinline__ float weights16(const uint32_t* s, float k, float add, int lim, uint32_t* pk) {
+  const uint64_t kk = f32x2(k, k), aa = f32x2(add, add);
+  uint64_t sum = 0;  // two f32 zeros
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    float2 x = f32x2_parts(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kk, aa));
+    if (EDGE) {
+      x.x = e < lim ? x.x : -INFINITY;
+      x.y = e + 1 < lim ? x.y : -INFINITY;
+    }
+    const float w0 = ex2_approx(x.x), w1 = ex2_approx(x.y);
+    sum = add_f32x2(sum, f32x2(w0, w1));
+    pk[e / 2] = F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
+  }
+  const float2 t = f32x2_parts(sum);
+  return t.x + t.y;
+}
 
 template <int D, bool F8>
 struct PreCfg {
@@ -50,11 +100,6 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
   return h;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Adds the values of positions [s0, s1) that are not finite to a row's output
 // (the tiles held zeros in their place, because other rows do not see them).
 template <int D, bool F8>
@@ -223,7 +268,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const uint64_t vd = make_smem_desc(smem_u32(ring), C::kSlabBytes, 1024, kSwizzle128B);
       const auto qk = [&](int q, int i) {
         const uint64_t a0 = qd + q * (C::kEntry >> 4), b0 = kd + (2 * i % kRing) * (C::kEntry >> 4);
-#pragma unroll 1
+#pragma unroll 4
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (C::kSlabBytes >> 4) + (k & 3) * 2;
           umma_bf16_ss(tmem + q * 128, a0 + off, b0 + off, idesc_qk, k != 0);
@@ -232,7 +277,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       };
       const auto pv = [&](int q, int i) {
         const uint64_t b0 = vd + ((2 * i + 1) % kRing) * (C::kEntry >> 4);
-#pragma unroll 1
+#pragma unroll 4
         for (int k = 0; k < kTile / 16; ++k)
           umma_bf16_ts(tmem + 256 + q * D, tmem + q * 128 + k * 8, b0 + k * (2048 >> 4), idesc_pv, (i | k) != 0);
       };
@@ -398,6 +443,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 
     float ref = -INFINITY, l = 0.f;  // reference exponent, sum of 2^(score - ref)
+    float vmax = -INFINITY;          // largest log2 of a V scale so far
     const int nt = q ? (u.nq > 1 ? n_tiles : 0) : n0;
     bool ok = true;
     for (int i = 0; i < nt && ok; ++i) {
@@ -409,6 +455,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (!ok) break;
       tc_fence_after();
       const float4* mt = meta + i % kMetas * 8;
+      if (F8)
+        for (int j = 0; j < p.ppt; ++j) vmax = fmaxf(vmax, mt[j].y);
       bool find = __any_sync(0xffffffffu, ref == -INFINITY && lim > 0);
       uint32_t pk[64];
       float sum;
@@ -453,44 +501,35 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           }
         }
         const float mu = ref == -INFINITY ? 0.f : ref;
-        float high = -INFINITY;
+        float high = 0.f;
         sum = 0.f;
+        uint32_t sb[2][32];
+        tmem_ld32<32>(ts, sb[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld32<32>(ts + c * 32, s);
           tmem_ld_wait();
+          if (c < 3) tmem_ld32<32>(ts + (c + 1) * 32, sb[(c + 1) & 1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const uint32_t* x = sb[c & 1] + h * 16;
             float k = cr, add = -mu, inv = 1.f;
+            bool thin = false;
             if constexpr (F8) {
               const float4 sc = mt[(c * 32 + h * 16) >> p.shift];
               k = cr * sc.x;
               add = sc.y - mu;
               inv = sc.z;
+              thin = sc.y < vmax - 90.f;
             }
-            float x[16], part = 0.f, big = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              x[e] = fmaf(__uint_as_float(s[h * 16 + e]), k, add);
-              if (edge && c * 32 + h * 16 + e >= lim) x[e] = -INFINITY;
-              big = fmaxf(big, x[e]);
-            }
-            high = fmaxf(high, big);
-            float w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = ex2_approx(x[e]);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              part += w[e] + w[e + 1];
-              pk[c * 16 + h * 8 + e / 2] = F8 ? pack_f16(w[e], w[e + 1]) : pack_bf16(w[e], w[e + 1]);
-            }
+            const int left = lim - (c * 32 + h * 16);
+            uint32_t* dst = pk + c * 16 + h * 8;
+            float part = edge ? weights16<F8, true>(x, k, add, left, dst) : weights16<F8, false>(x, k, add, left, dst);
+            high = fmaxf(high, part);
             if constexpr (F8) {
-              // weights that the V scale makes tiny, but not their share of the sum
-              if (big < -60.f && big > -INFINITY) {
+              if (thin) {  // a V scale that would flush the weights, not their share of the sum
                 part = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) part += ex2_approx(x[e] - (add + mu));
+                for (int e = 0; e < 16; ++e) part += e < left ? ex2_approx(fmaf(__uint_as_float(x[e]), k, -mu)) : 0.f;
               } else {
                 part *= inv;
               }
@@ -498,7 +537,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             sum += part;
           }
         }
-        if (!__any_sync(0xffffffffu, high > kLazy)) break;
+        if (!__any_sync(0xffffffffu, high > kMostSum)) break;
         find = true;
       }
       l += sum;
