@@ -242,7 +242,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = static_cast<uint32_t>(warp_uniform(static_cast<int>(*tmem_slot)));
   const uint32_t tmem_o = tmem + 2 * C::kN;
   pdl_trigger();
   pdl_wait();
@@ -316,53 +316,55 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ---------------------------------------------------------------- MMA
     constexpr uint32_t idesc_qk = F8 ? make_idesc_f8(128, C::kN, 0, 0) : make_idesc_bf16(128, C::kN, 0, 0);
     constexpr uint32_t idesc_pv = F8 ? make_idesc_f8(128, C::kN, 1, 0) : make_idesc_bf16(128, C::kN, 1, 0);
-    const uint32_t q_base = smem_u32(q_smem);
+    const bool lead = elect_one();
+    const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
+    // descriptors differ in the start address alone (16-byte units, low bits)
+    const uint64_t qd = make_smem_desc(smem_u32(q_smem), 16, 8 * C::kRowB, C::kSwz);
+    const uint64_t kd = make_smem_desc(smem_u32(ring), 16, 8 * C::kRowB, C::kSwz);
+    // V is MN-major: D on the rows.  D = 64 fills only half of the 128 rows;
+    // the second half repeats it (stride 0) and is not read.
+    const uint64_t vd = make_smem_desc(smem_u32(ring), D == 128 ? C::kSlabBytes : 0, 8 * C::kRowB, C::kSwz);
+    const uint64_t pd = make_smem_desc(smem_u32(p_smem), 16, 1024, kSwizzle128B);
     int it = 0, seg = 0;
     bool ok = true;
     const auto qk = [&](int t) {  // S(t) = K(t) Q^T
       const int e = 2 * t, st = e % kRing;
-      if (!mbar_wait(&full[st], (e / kRing) & 1, abort_flag)) return false;
+      if (!wait_all(&full[st], (e / kRing) & 1)) return false;
       tc_fence_after();
-      const uint32_t kb = smem_u32(ring + st * C::kEntry);
+      const uint64_t k0 = kd + st * (C::kEntry >> 4);
 #pragma unroll
       for (int k = 0; k < C::kRow / 32; ++k) {
         constexpr int kPer = C::kRowB / 32;
-        const uint64_t ad = make_smem_desc(kb + k / kPer * C::kSlabBytes + k % kPer * 32, 16, 8 * C::kRowB, C::kSwz);
-        const uint64_t bd = make_smem_desc(q_base + k / kPer * (C::kN * C::kRowB) + k % kPer * 32, 16, 8 * C::kRowB, C::kSwz);
-        if constexpr (F8) umma_f8_ss(tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
-        else umma_bf16_ss(tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
+        const uint64_t ad = k0 + (k / kPer * (C::kSlabBytes >> 4) + k % kPer * 2);
+        const uint64_t bd = qd + (k / kPer * (C::kN * C::kRowB >> 4) + k % kPer * 2);
+        if constexpr (F8) umma_f8_ss_by(lead, tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
+        else umma_f16_ss_by(lead, tmem + (t & 1) * C::kN, ad, bd, idesc_qk, k != 0);
       }
-      umma_commit(&empty[st]);
-      umma_commit(&s_full[t & 1]);
+      umma_commit_by(lead, &empty[st]);
+      umma_commit_by(lead, &s_full[t & 1]);
       return true;
     };
     while (ok && walk.next(s)) {
-      const int n = s.hi - s.lo;
-      if (lane == 0) {
-        ok = mbar_wait(q_full, seg & 1, abort_flag) && (n == 0 || qk(it));
-        for (int i = 0; ok && i < n; ++i) {
-          const int t = it + i;
-          if (i + 1 < n && !qk(t + 1)) { ok = false; break; }
-          const int e = 2 * t + 1, st = e % kRing;
-          ok = mbar_wait(&p_full[t & 1], (t >> 1) & 1, abort_flag) && mbar_wait(&full[st], (e / kRing) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vb = smem_u32(ring + st * C::kEntry), pb = smem_u32(p_smem + (t & 1) * C::kPBytes);
-          // V is MN-major: D on the rows.  D = 64 fills only half of the 128
-          // rows; the second half repeats it (stride 0) and is not read.
-          constexpr int kKeys = 32 / C::kElem;  // keys per MMA
+      const int n = warp_uniform(s.hi - s.lo);
+      ok = wait_all(q_full, seg & 1) && (n == 0 || qk(it));
+      for (int i = 0; ok && i < n; ++i) {
+        const int t = it + i;
+        if (i + 1 < n && !qk(t + 1)) { ok = false; break; }
+        const int e = 2 * t + 1, st = e % kRing;
+        ok = wait_all(&p_full[t & 1], (t >> 1) & 1) && wait_all(&full[st], (e / kRing) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t v0 = vd + st * (C::kEntry >> 4), p0 = pd + (t & 1) * (C::kPBytes >> 4);
+        constexpr int kKeys = 32 / C::kElem;  // keys per MMA
 #pragma unroll
-          for (int k = 0; k < kTile / kKeys; ++k) {
-            const uint64_t ad = make_smem_desc(vb + k * kKeys * C::kRowB, D == 128 ? C::kSlabBytes : 0, 8 * C::kRowB, C::kSwz);
-            const uint64_t bd = make_smem_desc(pb + k / 4 * (C::kN * 128) + k % 4 * 32, 16, 1024, kSwizzle128B);
-            if constexpr (F8) umma_f8_ss(tmem_o, ad, bd, idesc_pv, (i | k) != 0);
-            else umma_bf16_ss(tmem_o, ad, bd, idesc_pv, (i | k) != 0);
-          }
-          umma_commit(&empty[st]);
-          umma_commit(&pv_done[t & 1]);
+        for (int k = 0; k < kTile / kKeys; ++k) {
+          const uint64_t ad = v0 + k * (kKeys * C::kRowB >> 4), bd = p0 + (k / 4 * (C::kN * 128 >> 4) + k % 4 * 2);
+          if constexpr (F8) umma_f8_ss_by(lead, tmem_o, ad, bd, idesc_pv, (i | k) != 0);
+          else umma_f16_ss_by(lead, tmem_o, ad, bd, idesc_pv, (i | k) != 0);
         }
+        umma_commit_by(lead, &empty[st]);
+        umma_commit_by(lead, &pv_done[t & 1]);
       }
-      ok = __all_sync(0xffffffffu, ok);
       it += n;
       ++seg;
     }

@@ -17,7 +17,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = 128, kHalf = 64;  // keys of a loaded tile, and of a step of the products and the softmax
 constexpr int kMetas = 8;
 constexpr int kStages = 2;     // staging tiles of an 8-bit cache
 constexpr int kRing = 4;       // operand tiles: K, V, K, V
@@ -56,25 +56,61 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Sixteen weights of a row: 2^(score * k + add), zero from column lim - col on
-// (EDGE), rounded and packed two to a word.  Returns their f32 sum.
-template <bool F8, bool EDGE>
-__device__ __forceinline__ float weights16(const uint32_t* s, float k, float add, int lim, uint32_t* pk) {
-  const uint64_t kk = f32x2(k, k), aa = f32x2(add, add);
-  uint64_t sum = 0;  // two f32 zeros
+// The weights of a row over half a tile, 2^(score * k + add), rounded and packed two
+// to a word in pk; sum: their f32 sum in units of the row's reference; high: the
+// largest sum of sixteen.  GENERAL: columns from lim on are masked, and a V
+// scale so small that it would flush the weights (thin: below vmax by 2^90)
+// does not flush their share of the sum.  The other case has no branches, so
+// that the 64 exponentials overlap.
+template <bool F8, bool GENERAL>
+__device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int shift, float cr, float mu, int lim, float vmax,
+                                             uint32_t (&pk)[32], float& sum, float& high) {
+  sum = 0.f;
+  high = 0.f;
+  uint32_t sb[2][32];
+  tmem_ld32<32>(ts, sb[0]);
+  tmem_ld32<32>(ts + 32, sb[1]);
+  tmem_ld_wait();
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    float2 x = f32x2_parts(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kk, aa));
-    if (EDGE) {
-      x.x = e < lim ? x.x : -INFINITY;
-      x.y = e + 1 < lim ? x.y : -INFINITY;
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t* s = sb[c] + h * 16;
+      float k = cr, add = -mu, inv = 1.f;
+      bool thin = false;
+      if constexpr (F8) {
+        const float4 sc = mt[(c * 32 + h * 16) >> shift];
+        k = cr * sc.x;
+        add = sc.y - mu;
+        inv = sc.z;
+        thin = GENERAL && sc.y < vmax - 90.f;
+      }
+      const int left = lim - (c * 32 + h * 16);
+      const uint64_t kk = f32x2(k, k), aa = f32x2(add, add);
+      uint64_t acc[2] = {0, 0};  // f32 zeros
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float2 x = f32x2_parts(fma_f32x2(f32x2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), kk, aa));
+        if (GENERAL) {
+          x.x = e < left ? x.x : -INFINITY;
+          x.y = e + 1 < left ? x.y : -INFINITY;
+        }
+        const float w0 = ex2_approx(x.x), w1 = ex2_approx(x.y);
+        acc[e / 2 & 1] = add_f32x2(acc[e / 2 & 1], f32x2(w0, w1));
+        pk[c * 16 + h * 8 + e / 2] = F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
+      }
+      const float2 t = f32x2_parts(add_f32x2(acc[0], acc[1]));
+      float part = t.x + t.y;
+      high = fmaxf(high, part);
+      if (thin) {
+        part = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part += e < left ? ex2_approx(fmaf(__uint_as_float(s[e]), k, -mu)) : 0.f;
+        inv = 1.f;
+      }
+      sum = F8 ? fmaf(part, inv, sum) : sum + part;
     }
-    const float w0 = ex2_approx(x.x), w1 = ex2_approx(x.y);
-    sum = add_f32x2(sum, f32x2(w0, w1));
-    pk[e / 2] = F8 ? pack_f16(w0, w1) : pack_bf16(w0, w1);
   }
-  const float2 t = f32x2_parts(sum);
-  return t.x + t.y;
 }
 
 template <int D, bool F8>
@@ -85,7 +121,7 @@ struct PreCfg {
   static constexpr int kStage = F8 ? kTile * D : 0;
   static constexpr int kMetaBytes = kMetas * 8 * 16;
   static constexpr int kSmem = 1024 + (2 + kRing) * kEntry + kStages * kStage + kMetaBytes +
-                               8 * (2 * kRing + 2 * kStages + kMetas + 9) + 32;
+                               8 * (2 * kRing + 2 * kStages + kMetas + 16) + 32;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -131,7 +167,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, 1 / V scale
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(meta) + C::kMetaBytes);
   uint64_t *full = bars, *empty = full + kRing, *st_full = empty + kRing, *st_empty = st_full + kStages;
-  uint64_t *meta_full = st_empty + kStages, *s_full = meta_full + kMetas, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *meta_full = st_empty + kStages;
+  uint64_t *s_full = meta_full + kMetas, *p_full = s_full + 4, *pv_done = p_full + 4, *o_full = pv_done + 4;  // [Q tile][half]
   uint64_t *q_full = o_full + 1, *v_fixed = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_fixed + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -142,7 +179,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], F8 ? 4 : 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < kStages; ++i) { mbar_init(&st_full[i], 1); mbar_init(&st_empty[i], 4); }
     for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); }
+    for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
     mbar_init(o_full, 1);
     mbar_init(q_full, kSoftWarps);
     mbar_init(&v_fixed[0], 4);
@@ -158,7 +195,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = static_cast<uint32_t>(warp_uniform(static_cast<int>(*tmem_slot)));
   pdl_trigger();
   pdl_wait();
 
@@ -257,64 +294,69 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           if (mbar_try_wait(smem_u32(F8 ? &st_full[st] : &full[st]), ((2 * i - 1 - st) / kDepth) & 1)) break;
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && n_tiles > 0) {
+    const int n_tiles_ = warp_uniform(n_tiles), n0_ = warp_uniform(n0), nq = warp_uniform(u.nq);
+    if (n_tiles_ > 0) {
+      const bool lead = elect_one();
+      const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
       constexpr uint32_t fmt = F8 ? 0u : (1u << 7) | (1u << 10);
-      constexpr uint32_t idesc_qk = (make_idesc_bf16(128, kTile, 0, 0) & ~((1u << 7) | (1u << 10))) | fmt;
+      constexpr uint32_t idesc_qk = (make_idesc_bf16(128, kHalf, 0, 0) & ~((1u << 7) | (1u << 10))) | fmt;
       constexpr uint32_t idesc_pv = (make_idesc_bf16(128, D, 0, 1) & ~((1u << 7) | (1u << 10))) | fmt;
       const uint32_t qb = smem_u32(q_smem);
       // descriptors differ in the start address alone (16-byte units, low bits)
       const uint64_t qd = make_smem_desc(qb, 16, 1024, kSwizzle128B);
       const uint64_t kd = make_smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
       const uint64_t vd = make_smem_desc(smem_u32(ring), C::kSlabBytes, 1024, kSwizzle128B);
-      const auto qk = [&](int q, int i) {
-        const uint64_t a0 = qd + q * (C::kEntry >> 4), b0 = kd + (2 * i % kRing) * (C::kEntry >> 4);
-#pragma unroll 4
+      const auto qk = [&](int q, int i, int h) {  // S of half h: its keys are rows 64 h on of the tile
+        const uint64_t a0 = qd + q * (C::kEntry >> 4), b0 = kd + (2 * i % kRing) * (C::kEntry >> 4) + h * (kHalf * 128 >> 4);
+#pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * (C::kSlabBytes >> 4) + (k & 3) * 2;
-          umma_bf16_ss(tmem + q * 128, a0 + off, b0 + off, idesc_qk, k != 0);
+          umma_f16_ss_by(lead, tmem + q * 128 + h * kHalf, a0 + off, b0 + off, idesc_qk, k != 0);
         }
-        umma_commit(&s_full[q]);
+        umma_commit_by(lead, &s_full[2 * q + h]);
       };
-      const auto pv = [&](int q, int i) {
-        const uint64_t b0 = vd + ((2 * i + 1) % kRing) * (C::kEntry >> 4);
-#pragma unroll 4
-        for (int k = 0; k < kTile / 16; ++k)
-          umma_bf16_ts(tmem + 256 + q * D, tmem + q * 128 + k * 8, b0 + k * (2048 >> 4), idesc_pv, (i | k) != 0);
+      const auto pv = [&](int q, int i, int h) {
+        const uint64_t b0 = vd + ((2 * i + 1) % kRing) * (C::kEntry >> 4) + h * (kHalf * 128 >> 4);
+#pragma unroll
+        for (int k = 0; k < kHalf / 16; ++k)
+          umma_f16_ts_by(lead, tmem + 256 + q * D, tmem + q * 128 + h * kHalf + k * 8, b0 + k * (2048 >> 4), idesc_pv, (i | h | k) != 0);
+        umma_commit_by(lead, &pv_done[2 * q + h]);
       };
-      const auto wait_tile = [&](int e) { return mbar_wait(&full[e % kRing], (e / kRing) & 1, abort_flag); };
-      bool ok = mbar_wait(q_full, 0, abort_flag) && wait_tile(0);
+      const auto wait_tile = [&](int e) { return wait_all(&full[e % kRing], (e / kRing) & 1); };
+      bool ok = wait_all(q_full, 0) && wait_tile(0);
       if (ok) {
         tc_fence_after();
-        if (n0 > 0) qk(0, 0);
-        if (u.nq > 1) qk(1, 0);
-        umma_commit(&empty[0]);
+        for (int h = 0; h < 2; ++h) {
+          if (n0_ > 0) qk(0, 0, h);
+          if (nq > 1) qk(1, 0, h);
+        }
+        umma_commit_by(lead, &empty[0]);
       }
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        const int st = (2 * i + 1) % kRing;
-        for (int q = 0; q < u.nq && ok; ++q) {
-          const int nq = q ? n_tiles : n0;
-          if (i < nq) {
-            ok = mbar_wait(&p_full[q], i & 1, abort_flag);
-            if (q == 0 || i >= n0) {
-              ok = ok && (F8 ? wait_tile(2 * i + 1) : mbar_wait(&v_fixed[i & 1], (i >> 1) & 1, abort_flag));
-            }
+      // Each half of S is refilled as soon as its weights have been used, while
+      // the softmax works on the other half.
+      for (int i = 0; i < n_tiles_ && ok; ++i) {
+        for (int hq = 0; hq < 2 * nq && ok; ++hq) {
+          const int h = hq / nq, q = hq % nq, nt = q ? n_tiles_ : n0_;
+          if (i < nt) {
+            ok = wait_all(&p_full[2 * q + h], i & 1);
+            if (h == 0 && (q == 0 || i >= n0_)) ok = ok && (F8 ? wait_tile(2 * i + 1) : wait_all(&v_fixed[i & 1], (i >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            pv(q, i);
+            pv(q, i, h);
           }
-          if (i + 1 < n_tiles) {
-            if (q == 0) {
+          if (i + 1 < n_tiles_) {
+            if (hq == 0) {
               ok = wait_tile(2 * i + 2);
               tc_fence_after();
             }
-            if (ok && i + 1 < nq) qk(q, i + 1);
+            if (ok && i + 1 < nt) qk(q, i + 1, h);
           }
         }
         if (!ok) break;
-        umma_commit(&empty[st]);
-        if (i + 1 < n_tiles) umma_commit(&empty[(2 * i + 2) % kRing]);
+        umma_commit_by(lead, &empty[(2 * i + 1) % kRing]);
+        if (i + 1 < n_tiles_) umma_commit_by(lead, &empty[(2 * i + 2) % kRing]);
       }
-      if (ok) umma_commit(o_full);
+      if (ok) umma_commit_by(lead, o_full);
     }
   } else if (warp < kTmaWarp) {
     // ---------------------------------------------------------------- 8-bit tiles to f16; V slots past the rows
@@ -446,36 +488,41 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     float vmax = -INFINITY;          // largest log2 of a V scale so far
     const int nt = q ? (u.nq > 1 ? n_tiles : 0) : n0;
     bool ok = true;
-    for (int i = 0; i < nt && ok; ++i) {
-      const int lim = t - (u.lo + i) * kTile;  // keys of the tile that the row sees
-      const bool edge = __any_sync(0xffffffffu, lim < kTile);
+    bool thin = false;  // a page of the tile has a V scale far below the others'
+    for (int g = 0; g < 2 * nt && ok; ++g) {
+      const int i = g >> 1, h = g & 1;
+      const int lim = t - (u.lo + i) * kTile - h * kHalf;  // keys of the half that the row sees
+      const bool edge = __any_sync(0xffffffffu, lim < kHalf);
       if (F8) ok = mbar_wait(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag);
-      ok = mbar_wait(&s_full[q], i & 1, abort_flag) && ok;
+      ok = mbar_wait(&s_full[2 * q + h], i & 1, abort_flag) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const float4* mt = meta + i % kMetas * 8;
-      if (F8)
+      const uint32_t th = ts + h * kHalf;
+      const float4* mt = meta + i % kMetas * 8 + (h ? kHalf >> p.shift : 0);  // (a page of 128: its only entry)
+      if (F8 && h == 0) {
         for (int j = 0; j < p.ppt; ++j) vmax = fmaxf(vmax, mt[j].y);
+        thin = false;
+        for (int j = 0; j < p.ppt; ++j) thin = thin || mt[j].y < vmax - 90.f;
+      }
       bool find = __any_sync(0xffffffffu, ref == -INFINITY && lim > 0);
-      uint32_t pk[64];
+      uint32_t pk[32];
       float sum;
       while (true) {
         if (find) {  // the rows' maxima first
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t s[32];
-            tmem_ld32<32>(ts + c * 32, s);
+            tmem_ld32<32>(th + c * 32, s);
             tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int e0 = 0; e0 < 32; e0 += 16) {
               float part = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                part = fmaxf(part, !edge || c * 32 + h * 16 + e < lim ? __uint_as_float(s[h * 16 + e]) : -INFINITY);
+              for (int e = e0; e < e0 + 16; ++e) part = fmaxf(part, c * 32 + e < lim ? __uint_as_float(s[e]) : -INFINITY);
               if constexpr (F8) {
-                const float4 sc = mt[(c * 32 + h * 16) >> p.shift];
+                const float4 sc = mt[(c * 32 + e0) >> p.shift];
                 part = part == -INFINITY ? part : fmaf(part, cr * sc.x, sc.y);
               } else {
                 part *= cr;
@@ -487,7 +534,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           const float f = next == ref ? 1.f : ex2_approx(ref - next);
           ref = next;
           l *= f;
-          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // O of the tiles before is complete (products finish in order)
+          if (g > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // once the product of the half before has been added
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[2 * q + (h ^ 1)], ((g - 1) >> 1) & 1, abort_flag));
+            tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -501,52 +550,18 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           }
         }
         const float mu = ref == -INFINITY ? 0.f : ref;
-        float high = 0.f;
-        sum = 0.f;
-        uint32_t sb[2][32];
-        tmem_ld32<32>(ts, sb[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          if (c < 3) tmem_ld32<32>(ts + (c + 1) * 32, sb[(c + 1) & 1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t* x = sb[c & 1] + h * 16;
-            float k = cr, add = -mu, inv = 1.f;
-            bool thin = false;
-            if constexpr (F8) {
-              const float4 sc = mt[(c * 32 + h * 16) >> p.shift];
-              k = cr * sc.x;
-              add = sc.y - mu;
-              inv = sc.z;
-              thin = sc.y < vmax - 90.f;
-            }
-            const int left = lim - (c * 32 + h * 16);
-            uint32_t* dst = pk + c * 16 + h * 8;
-            float part = edge ? weights16<F8, true>(x, k, add, left, dst) : weights16<F8, false>(x, k, add, left, dst);
-            high = fmaxf(high, part);
-            if constexpr (F8) {
-              if (thin) {  // a V scale that would flush the weights, not their share of the sum
-                part = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) part += e < left ? ex2_approx(fmaf(__uint_as_float(x[e]), k, -mu)) : 0.f;
-              } else {
-                part *= inv;
-              }
-            }
-            sum += part;
-          }
-        }
+        float high;
+        if (edge || thin) tile_weights<F8, true>(th, mt, p.shift, cr, mu, lim, vmax, pk, sum, high);
+        else tile_weights<F8, false>(th, mt, p.shift, cr, mu, lim, vmax, pk, sum, high);
         if (!__any_sync(0xffffffffu, high > kMostSum)) break;
         find = true;
       }
       l += sum;
-      tmem_st32x32(ts, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-      tmem_st32x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+      tmem_st32x32(th, pk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[q]);
+      if (lane == 0) mbar_arrive(&p_full[2 * q + h]);
     }
     // ---- output
     if (ok && nt > 0) ok = mbar_wait(o_full, 0, abort_flag);
