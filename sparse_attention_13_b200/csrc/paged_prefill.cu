@@ -368,36 +368,41 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         ok = mbar_wait(&st_full[st], (e / kStages) & 1, abort_flag) && mbar_wait(&empty[rg], ((e / kRing) & 1) ^ 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint8_t* src = stage + st * C::kStage;
-        uint8_t* dst = ring + rg * C::kEntry;
-        const bool look = (e & 1) && i >= fix;
-        constexpr int kChunks = D / 16;  // 16-byte chunks of a staged row
-#pragma unroll 2
-        for (int j = 0; j < kTile * kChunks / 128; ++j) {
-          const int c = j * 128 + tid, row = c / kChunks, cc = c % kChunks;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + c * 16);
-          uint32_t x[4] = {w.x, w.y, w.z, w.w};
-          if (look) {
-            const int pos = (u.lo + i) * kTile + row;
-            if (pos >= u.t0) {
+        // A thread widens the same 16 columns of every (128 / kChunks)-th row:
+        // its place in the swizzled rows is fixed.  The upper slab's lanes
+        // store their second chunk first, so that eight lanes cover all banks.
+        constexpr int kChunks = D / 16, kRows = 128 / kChunks, kSteps = kTile / kRows, kBatch = 4;
+        const int row0 = tid / kChunks, cc = tid % kChunks;
+        const bool flip = cc & 4;
+        const uint8_t* src = stage + st * C::kStage + tid * 16;
+        uint8_t* d = ring + rg * C::kEntry + cc / 4 * C::kSlabBytes + row0 * 128;
+        const int ch = cc % 4 * 2;
+        uint8_t *d0 = d + (((ch + flip) ^ (row0 & 7)) << 4), *d1 = d + (((ch + 1 - flip) ^ (row0 & 7)) << 4);
+        const int look = (e & 1) && i >= fix ? u.t0 - (u.lo + i) * kTile : kTile;  // rows from here on need a look
+#pragma unroll
+        for (int j0 = 0; j0 < kSteps; j0 += kBatch) {
+          uint4 w[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) w[j] = *reinterpret_cast<const uint4*>(src + (j0 + j) * kRows * D);
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+            const int row = row0 + (j0 + j) * kRows;
+            if (row >= look) {
+              const bool gone = (u.lo + i) * kTile + row >= u.t1;
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
                 const uint32_t nan = __vcmpeq4(x[v] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                if (nan && pos < u.t1) *poison = 1;
-                x[v] = pos < u.t1 ? x[v] & ~nan : 0u;
+                if (nan && !gone) *poison = 1;
+                x[v] = gone ? 0u : x[v] & ~nan;
               }
             }
+            const uint32_t a0 = flip ? x[2] : x[0], a1 = flip ? x[3] : x[1], b0 = flip ? x[0] : x[2], b1 = flip ? x[1] : x[3];
+            *reinterpret_cast<uint4*>(d0 + (j0 + j) * kRows * 128) =
+                make_uint4(f16x2_of_e4m3x2(a0 & 0xffffu), f16x2_of_e4m3x2(a0 >> 16), f16x2_of_e4m3x2(a1 & 0xffffu), f16x2_of_e4m3x2(a1 >> 16));
+            *reinterpret_cast<uint4*>(d1 + (j0 + j) * kRows * 128) =
+                make_uint4(f16x2_of_e4m3x2(b0 & 0xffffu), f16x2_of_e4m3x2(b0 >> 16), f16x2_of_e4m3x2(b1 & 0xffffu), f16x2_of_e4m3x2(b1 >> 16));
           }
-          uint32_t y[8];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            y[2 * v] = f16x2_of_e4m3x2(x[v] & 0xffffu);
-            y[2 * v + 1] = f16x2_of_e4m3x2(x[v] >> 16);
-          }
-          uint8_t* d = dst + cc / 4 * C::kSlabBytes + row * 128;
-          const int ch = cc % 4 * 2;
-          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
