@@ -121,7 +121,7 @@ struct PreCfg {
   static constexpr int kStage = F8 ? kTile * D : 0;
   static constexpr int kMetaBytes = kMetas * 8 * 16;
   static constexpr int kSmem = 1024 + (2 + kRing) * kEntry + kStages * kStage + kMetaBytes +
-                               8 * (2 * kRing + 2 * kStages + kMetas + 16) + 32;
+                               8 * (2 * kRing + 2 * kStages + kMetas + 17) + 32;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -169,18 +169,19 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   uint64_t *full = bars, *empty = full + kRing, *st_full = empty + kRing, *st_empty = st_full + kStages;
   uint64_t *meta_full = st_empty + kStages;
   uint64_t *s_full = meta_full + kMetas, *p_full = s_full + 4, *pv_done = p_full + 4, *o_full = pv_done + 4;  // [Q tile][half]
-  uint64_t *q_full = o_full + 1, *v_fixed = q_full + 1;
+  uint64_t *q_full = o_full + 2, *v_fixed = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_fixed + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* poison = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], F8 ? 4 : 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], F8 ? 4 : 1); mbar_init(&empty[i], 2); }
     for (int i = 0; i < kStages; ++i) { mbar_init(&st_full[i], 1); mbar_init(&st_empty[i], 4); }
     for (int i = 0; i < kMetas; ++i) mbar_init(&meta_full[i], 1);
     for (int i = 0; i < 4; ++i) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 4); mbar_init(&pv_done[i], 1); }
-    mbar_init(o_full, 1);
+    mbar_init(&o_full[0], 1);
+    mbar_init(&o_full[1], 1);
     mbar_init(q_full, kSoftWarps);
     mbar_init(&v_fixed[0], 4);
     mbar_init(&v_fixed[1], 4);
@@ -293,8 +294,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         for (int w = 0; w < 64 && 2 * i > st; ++w)
           if (mbar_try_wait(smem_u32(F8 ? &st_full[st] : &full[st]), ((2 * i - 1 - st) / kDepth) & 1)) break;
     }
-  } else if (warp == kMmaWarp) {
-    const int n_tiles_ = warp_uniform(n_tiles), n0_ = warp_uniform(n0), nq = warp_uniform(u.nq);
+  } else if (warp >= kMmaWarp && warp < kMmaWarp + 2) {
+    // One warp per Q tile: while one sets up its next products, the other's run.
+    const int q = warp - kMmaWarp;
+    const int n_tiles_ = warp_uniform(n_tiles), nt = warp_uniform(q ? (u.nq > 1 ? n_tiles : 0) : n0);
     if (n_tiles_ > 0) {
       const bool lead = elect_one();
       const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
@@ -306,7 +309,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       const uint64_t qd = make_smem_desc(qb, 16, 1024, kSwizzle128B);
       const uint64_t kd = make_smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
       const uint64_t vd = make_smem_desc(smem_u32(ring), C::kSlabBytes, 1024, kSwizzle128B);
-      const auto qk = [&](int q, int i, int h) {  // S of half h: its keys are rows 64 h on of the tile
+      const auto qk = [&](int i, int h) {  // S of half h: its keys are rows 64 h on of the tile
         const uint64_t a0 = qd + q * (C::kEntry >> 4), b0 = kd + (2 * i % kRing) * (C::kEntry >> 4) + h * (kHalf * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -315,7 +318,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         umma_commit_by(lead, &s_full[2 * q + h]);
       };
-      const auto pv = [&](int q, int i, int h) {
+      const auto pv = [&](int i, int h) {
         const uint64_t b0 = vd + ((2 * i + 1) % kRing) * (C::kEntry >> 4) + h * (kHalf * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < kHalf / 16; ++k)
@@ -326,37 +329,33 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       bool ok = wait_all(q_full, 0) && wait_tile(0);
       if (ok) {
         tc_fence_after();
-        for (int h = 0; h < 2; ++h) {
-          if (n0_ > 0) qk(0, 0, h);
-          if (nq > 1) qk(1, 0, h);
-        }
+        if (nt > 0) { qk(0, 0); qk(0, 1); }
         umma_commit_by(lead, &empty[0]);
       }
       // Each half of S is refilled as soon as its weights have been used, while
-      // the softmax works on the other half.
+      // the softmax works on the other half.  Tiles that this Q tile does not
+      // need are released all the same.
       for (int i = 0; i < n_tiles_ && ok; ++i) {
-        for (int hq = 0; hq < 2 * nq && ok; ++hq) {
-          const int h = hq / nq, q = hq % nq, nt = q ? n_tiles_ : n0_;
-          if (i < nt) {
-            ok = wait_all(&p_full[2 * q + h], i & 1);
-            if (h == 0 && (q == 0 || i >= n0_)) ok = ok && (F8 ? wait_tile(2 * i + 1) : wait_all(&v_fixed[i & 1], (i >> 1) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            pv(q, i, h);
-          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (i < nt) ok = ok && wait_all(&p_full[2 * q + h], i & 1);
+          if (h == 0) ok = ok && (F8 ? wait_tile(2 * i + 1) : wait_all(&v_fixed[i & 1], (i >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (i < nt) pv(i, h);
           if (i + 1 < n_tiles_) {
-            if (hq == 0) {
+            if (h == 0) {
               ok = wait_tile(2 * i + 2);
               tc_fence_after();
             }
-            if (ok && i + 1 < nt) qk(q, i + 1, h);
+            if (ok && i + 1 < nt) qk(i + 1, h);
           }
         }
         if (!ok) break;
         umma_commit_by(lead, &empty[(2 * i + 1) % kRing]);
         if (i + 1 < n_tiles_) umma_commit_by(lead, &empty[(2 * i + 2) % kRing]);
       }
-      if (ok) umma_commit_by(lead, o_full);
+      if (ok) umma_commit_by(lead, &o_full[q]);
     }
   } else if (warp < kTmaWarp) {
     // ---------------------------------------------------------------- 8-bit tiles to f16; V slots past the rows
@@ -569,7 +568,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (lane == 0) mbar_arrive(&p_full[2 * q + h]);
     }
     // ---- output
-    if (ok && nt > 0) ok = mbar_wait(o_full, 0, abort_flag);
+    if (ok && nt > 0) ok = mbar_wait(&o_full[q], 0, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     if (ok && q < u.nq) {
       tc_fence_after();
