@@ -63,16 +63,16 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // does not flush their share of the sum.  The other case has no branches, so
 // that the 64 exponentials overlap.
 template <bool F8, bool GENERAL>
-__device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int shift, float cr, float mu, int lim, float vmax,
+__device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int shift, float cr, float mu, int lim,
                                              uint32_t (&pk)[32], float& sum, float& high) {
   sum = 0.f;
   high = 0.f;
   uint32_t sb[2][32];
   tmem_ld32<32>(ts, sb[0]);
-  tmem_ld32<32>(ts + 32, sb[1]);
-  tmem_ld_wait();
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
+    tmem_ld_wait();
+    if (c == 0) tmem_ld32<32>(ts + 32, sb[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t* s = sb[c] + h * 16;
@@ -83,7 +83,7 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int 
         k = cr * sc.x;
         add = sc.y - mu;
         inv = sc.z;
-        thin = GENERAL && sc.y < vmax - 90.f;
+        thin = GENERAL && (sc.w == 1.f || sc.w == 3.f);
       }
       const int left = lim - (c * 32 + h * 16);
       const uint64_t kk = f32x2(k, k), aa = f32x2(add, add);
@@ -164,7 +164,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   uint8_t* q_smem = smem;
   uint8_t* ring = q_smem + 2 * C::kEntry;
   uint8_t* stage = ring + kRing * C::kEntry;
-  float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, 1 / V scale
+  float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, 1 / V scale, flags
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(meta) + C::kMetaBytes);
   uint64_t *full = bars, *empty = full + kRing, *st_full = empty + kRing, *st_empty = st_full + kStages;
   uint64_t *meta_full = st_empty + kStages;
@@ -246,6 +246,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         vs = __ldg(p.a.v_scale + at);
       }
     };
+    float vmax = -INFINITY;  // largest log2 of a V scale so far
     int pg = -1, pn = -1;
     float ks = 1.f, vs = 1.f, kn = 1.f, vn = 1.f;
     if (n_tiles > 0) fetch(u.lo, pn, kn, vn);
@@ -270,7 +271,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         ok = __all_sync(0xffffffffu, mbar_wait(eb, ((e / kDepth) & 1) ^ 1, abort_flag));
         if (!ok) break;
         if (F8 && kv == 0) {
-          if (lane < p.ppt) meta[i % kMetas * 8 + lane] = make_float4(mk, __log2f(mv), __fdividef(1.f, mv), 0.f);
+          // w: 1 for a page whose V scale would flush the weights (thin), 2 more
+          // where the tile has such a page
+          const float lv = __log2f(mv);
+          vmax = fmaxf(vmax, warp_max_f32(lv));
+          const bool thin = lv < vmax - 90.f;
+          const float w = (thin ? 1.f : 0.f) + (__any_sync(0xffffffffu, thin) ? 2.f : 0.f);
+          if (lane < p.ppt) meta[i % kMetas * 8 + lane] = make_float4(mk, lv, __fdividef(1.f, mv), w);
           __syncwarp();
           if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
         }
@@ -300,7 +307,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int n_tiles_ = warp_uniform(n_tiles), nt = warp_uniform(q ? (u.nq > 1 ? n_tiles : 0) : n0);
     if (n_tiles_ > 0) {
       const bool lead = elect_one();
-      const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
+      const auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_spin(bar, parity, abort_flag)); };
       constexpr uint32_t fmt = F8 ? 0u : (1u << 7) | (1u << 10);
       constexpr uint32_t idesc_qk = (make_idesc_bf16(128, kHalf, 0, 0) & ~((1u << 7) | (1u << 10))) | fmt;
       constexpr uint32_t idesc_pv = (make_idesc_bf16(128, D, 0, 1) & ~((1u << 7) | (1u << 10))) | fmt;
@@ -452,7 +459,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const int tok = m / p.G, g = m - tok * p.G;
     const int row = q * p.tok + tok;               // row of the unit
     const bool live = tok < p.tok && row < u.rows;
-    const int t = live ? paged_visible(p.a, u.b, u.row0 - paged_first(p.a, u.b) + row, p.inclusive) : 0;
+    // (rows beyond the unit compute along with the last one and are not written)
+    const int t = paged_visible(p.a, u.b, u.row0 - paged_first(p.a, u.b) + min(row, max(0, u.rows - 1)), p.inclusive);
+    const int t_lo = __reduce_min_sync(0xffffffffu, t);
     const int64_t at = static_cast<int64_t>(u.row0 + row) * p.n_h + u.kvh * p.G + g;
     float cr = p.scale_log2;  // factor of the row's scores
     {
@@ -489,27 +498,22 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 
     float ref = -INFINITY, l = 0.f;  // reference exponent, sum of 2^(score - ref)
-    float vmax = -INFINITY;          // largest log2 of a V scale so far
     const int nt = q ? (u.nq > 1 ? n_tiles : 0) : n0;
     bool ok = true;
     bool thin = false;  // a page of the tile has a V scale far below the others'
     for (int g = 0; g < 2 * nt && ok; ++g) {
       const int i = g >> 1, h = g & 1;
       const int lim = t - (u.lo + i) * kTile - h * kHalf;  // keys of the half that the row sees
-      const bool edge = __any_sync(0xffffffffu, lim < kHalf);
-      if (F8) ok = mbar_wait(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag);
+      const bool edge = t_lo - (u.lo + i) * kTile - h * kHalf < kHalf;
+      if (F8 && h == 0) ok = mbar_wait(&meta_full[i % kMetas], (i / kMetas) & 1, abort_flag);
       ok = mbar_wait(&s_full[2 * q + h], i & 1, abort_flag) && ok;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t th = ts + h * kHalf;
       const float4* mt = meta + i % kMetas * 8 + (h ? kHalf >> p.shift : 0);  // (a page of 128: its only entry)
-      if (F8 && h == 0) {
-        for (int j = 0; j < p.ppt; ++j) vmax = fmaxf(vmax, mt[j].y);
-        thin = false;
-        for (int j = 0; j < p.ppt; ++j) thin = thin || mt[j].y < vmax - 90.f;
-      }
-      bool find = __any_sync(0xffffffffu, ref == -INFINITY && lim > 0);
+      if (F8 && h == 0) thin = mt[0].w >= 2.f;
+      bool find = g == 0;  // (a row that sees no key of the first half sees none)
       uint32_t pk[32];
       float sum;
       while (true) {
@@ -555,8 +559,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
         const float mu = ref == -INFINITY ? 0.f : ref;
         float high;
-        if (edge || thin) tile_weights<F8, true>(th, mt, p.shift, cr, mu, lim, vmax, pk, sum, high);
-        else tile_weights<F8, false>(th, mt, p.shift, cr, mu, lim, vmax, pk, sum, high);
+        if (edge || thin) tile_weights<F8, true>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
+        else tile_weights<F8, false>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
         if (!__any_sync(0xffffffffu, high > kMostSum)) break;
         find = true;
       }
