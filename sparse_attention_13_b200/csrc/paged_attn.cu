@@ -21,7 +21,7 @@ namespace dsa {
 namespace {
 
 constexpr int kTile = 128;         // keys per tile
-constexpr int kMaxCtas = 320;      // CTAs that may leave partial results
+constexpr int kMaxCtas = 480;      // CTAs that may leave partial results
 constexpr int kNoPage = 1 << 30;   // position of a slot that no page holds
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -159,14 +159,14 @@ struct Walker {
   }
 };
 
-template <int D, bool F8, int NH>
+template <int D, bool F8, int NH, bool SPARSE>
 struct Cfg {
   static constexpr int kHG = NH < 16 ? NH : 16;      // heads per epilogue group of four warps
   static constexpr int kGroups = NH / kHG;
   static constexpr int kEpiWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
   static constexpr int kThreads = 32 * (kEpiWarps + 2);
-  static constexpr int kCtasPerSm = NH <= 16 ? 2 : 1;
+  static constexpr int kCtasPerSm = SPARSE && NH == 8 && F8 ? 3 : NH <= 16 ? 2 : 1;
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kN = F8 ? 2 * NH : (NH < 16 ? 16 : NH);  // MMA columns
   static constexpr int kRow = D * kElem;                        // bytes of a cached row
@@ -177,14 +177,14 @@ struct Cfg {
   static constexpr int kEntry = kTile * kRow;                   // a K or V tile
   static constexpr int kQBytes = kN * kRow;
   static constexpr int kPBytes = kN * kTile * kElem;
-  static constexpr int kRing = (NH <= 16 ? 96 : 176) * 1024 / kEntry;  // entries: K, V, K, V, ...
+  static constexpr int kRing = (kCtasPerSm == 3 ? 64 : kCtasPerSm == 2 ? 96 : 176) * 1024 / kEntry;  // entries: K, V, K, V, ...
   static constexpr int kMetas = kRing / 2 + 3;  // a slot is rewritten only after the PV of its tile
   static constexpr int kMetaBytes = kMetas * 8 * 16;
   static constexpr int kWm = kGroups * 2 * 4 * (kHG + 4);
   static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
   static constexpr int kSmem = 1024 + kRing * kEntry + kQBytes + 2 * kPBytes + kMetaBytes + kWm * 4 + 2 * NH * 4 +
                                4 * NH * 4 + kEpiWarps * 4 * kHG * 4 + 8 * (2 * kRing + kMetas + 8) + 64;
-  static_assert(kSmem <= (kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
+  static_assert(kSmem <= (kCtasPerSm == 3 ? 75 : kCtasPerSm == 2 ? 113 : 227) * 1024, "shared memory");
 };
 
 // Byte offset of row n, byte column c of a K-major operand slab with rows of
@@ -199,10 +199,10 @@ __device__ __forceinline__ uint32_t op_off(int n, int c) {
 // = column of D in the output); then one TMA warp and one MMA warp.  Bound by
 // the cache's bytes for decode: the ring keeps 96 KB per CTA in flight.
 template <int D, bool F8, int NH, bool SPARSE>
-__global__ void __launch_bounds__(Cfg<D, F8, NH>::kThreads, Cfg<D, F8, NH>::kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, F8, NH, SPARSE>::kThreads, Cfg<D, F8, NH, SPARSE>::kCtasPerSm)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PattnParams p) {
-  using C = Cfg<D, F8, NH>;
+  using C = Cfg<D, F8, NH, SPARSE>;
   constexpr int HG = C::kHG, kRing = C::kRing, kMetas = C::kMetas;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -782,7 +782,10 @@ Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n
   pl.units = (n_sel ? static_cast<long long>(pb->total_q) : static_cast<long long>(pb->B) * pl.max_rb) * kv->n_kv * pl.hbs;
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
-  const int ctas = std::min(kMaxCtas, sms * (pl.NH <= 16 ? 2 : 1));
+  const int two = std::min(kMaxCtas, sms * (pl.NH <= 16 ? 2 : 1));
+  // many units of selected 8-bit pages run three CTAs to an SM (latency-bound:
+  // 1359 -> 1157 us for 16,384 units of 16 tiles)
+  const int ctas = n_sel && pl.NH == 8 && kv->fmt == DSA_KV_E4M3 && pl.units >= 8ll * two ? std::min(kMaxCtas, sms * 3) : two;
   pl.aligned = n_sel && pl.units >= 8ll * ctas;
   pl.grid = static_cast<int>(std::min<long long>(ctas, pl.aligned ? pl.units : std::max(1ll, pl.units * pl.tpu / 2)));
   pl.merge = !pl.aligned && pl.grid > 1;
@@ -796,7 +799,7 @@ Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n
 
 template <int D, bool F8, int NH, bool SPARSE>
 cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnParams& p, const Plan& pl, cudaStream_t s) {
-  using C = Cfg<D, F8, NH>;
+  using C = Cfg<D, F8, NH, SPARSE>;
   auto fn = paged_attn_kernel<D, F8, NH, SPARSE>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), C::kSmem);
   if (e == cudaSuccess) e = launch_pdl(fn, dim3(pl.grid), dim3(C::kThreads), C::kSmem, s, k, v, p);
