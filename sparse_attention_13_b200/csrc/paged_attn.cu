@@ -60,6 +60,9 @@ struct Walker {
   long long pos, end, total;
   long long base, weight;  // dense: first tile and tiles of the current sequence
   int b, r0, n, nrb, tiles;
+  // the unit that holds pos: its row or row block, head and head block, and
+  // pos's tile in it (kept by counting: no divisions on the way)
+  int at, kvh, hb, tile;
 
   __device__ __forceinline__ long long seq(int s, int& r, int& rows, int& blocks, int& t) const {
     paged_rows(p.a, s, r, rows);
@@ -75,6 +78,12 @@ struct Walker {
       total = units * p.tpu;
       pos = p.aligned ? units * c / C * p.tpu : total * c / C;
       end = p.aligned ? units * (c + 1) / C * p.tpu : total * (c + 1) / C;
+      const long long u = pos / p.tpu;
+      tile = static_cast<int>(pos - u * p.tpu);
+      at = static_cast<int>(u % p.a.total_q);
+      kvh = static_cast<int>(u / p.a.total_q) / p.hbs;
+      hb = static_cast<int>(u / p.a.total_q) % p.hbs;
+      b = -1;
     } else {
       const int lane = threadIdx.x & 31;
       int r, rows, blocks, t;
@@ -107,49 +116,61 @@ struct Walker {
         base += __shfl_sync(0xffffffffu, w, 31);
       }
       weight = b < p.a.B ? seq(b, r0, n, nrb, tiles) : 0;
+      if (weight) {
+        const long long u = (pos - base) / tiles;
+        tile = static_cast<int>(pos - base - u * tiles);
+        at = static_cast<int>(u % nrb);
+        kvh = static_cast<int>(u / nrb) / p.hbs;
+        hb = static_cast<int>(u / nrb) % p.hbs;
+      }
     }
   }
 
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
-    long long u, nominal;
+    int nominal;
     if constexpr (SPARSE) {
-      u = pos / p.tpu;
-      s.lo = static_cast<int>(pos - u * p.tpu);
       nominal = p.tpu;
-      s.unit = static_cast<int>(u);
-      s.row0 = static_cast<int>(u % p.a.total_q);
-      const int rem = static_cast<int>(u / p.a.total_q);
-      s.kvh = rem / p.hbs;
-      s.h0 = rem % p.hbs * p.Gx;
-      s.b = paged_seq(p.a, s.row0);
+      s.unit = (kvh * p.hbs + hb) * p.a.total_q + at;
+      s.row0 = at;
+      if (b < 0) b = paged_seq(p.a, at);
+      else if (p.a.one) b = at;
+      else while (b + 1 < p.a.B && __ldg(p.a.cu_q + b + 1) <= at) ++b;
       s.nr = 1;
-      s.t0 = s.t1 = paged_visible(p.a, s.b, s.row0 - paged_first(p.a, s.b), p.inclusive);
+      s.t0 = s.t1 = paged_visible(p.a, b, at - paged_first(p.a, b), p.inclusive);
     } else {
-      while (pos >= base + weight) {
+      while (pos >= base + weight) {  // (tile, at, kvh and hb are zero here)
         base += weight;
         weight = seq(++b, r0, n, nrb, tiles);
       }
-      u = (pos - base) / tiles;
-      s.lo = static_cast<int>(pos - base - u * tiles);
       nominal = tiles;
-      const int rb = static_cast<int>(u % nrb), rem = static_cast<int>(u / nrb);
-      s.kvh = rem / p.hbs;
-      s.h0 = rem % p.hbs * p.Gx;
-      s.b = b;
-      s.unit = ((b * p.a.n_kv + s.kvh) * p.hbs + rem % p.hbs) * p.max_rb + rb;
-      s.row0 = r0 + rb * p.R;
-      s.nr = min(p.R, n - rb * p.R);
-      s.t0 = paged_visible(p.a, b, rb * p.R, p.inclusive);
-      s.t1 = paged_visible(p.a, b, rb * p.R + s.nr - 1, p.inclusive);
+      s.unit = ((b * p.a.n_kv + kvh) * p.hbs + hb) * p.max_rb + at;
+      s.row0 = r0 + at * p.R;
+      s.nr = min(p.R, n - at * p.R);
+      s.t0 = paged_visible(p.a, b, at * p.R, p.inclusive);
+      s.t1 = paged_visible(p.a, b, at * p.R + s.nr - 1, p.inclusive);
     }
+    s.b = b;
+    s.kvh = kvh;
+    s.h0 = hb * p.Gx;
     s.nh = min(p.Gx, p.G - s.h0) * s.nr;
-    const long long left = end - pos;
-    s.hi = static_cast<int>(min(nominal, s.lo + left));
-    const long long unit_end = pos - s.lo + nominal;
-    pos += s.hi - s.lo;
+    s.lo = tile;
+    s.hi = static_cast<int>(min(static_cast<long long>(nominal), tile + (end - pos)));
     s.slot = s.lo == 0 ? (s.hi == nominal ? -1 : 1) : 0;
-    s.last_cta = static_cast<int>((unit_end * gridDim.x - 1) / total);
+    if (s.slot == 1) s.last_cta = static_cast<int>(((pos - s.lo + nominal) * gridDim.x - 1) / total);
+    pos += s.hi - s.lo;
+    tile = s.hi;
+    if (tile == nominal) {  // the next unit: rows within a head, heads within a sequence
+      tile = 0;
+      if (++at == (SPARSE ? p.a.total_q : nrb)) {
+        at = 0;
+        if (SPARSE) b = -1;
+        if (++hb == p.hbs) {
+          hb = 0;
+          if (++kvh == p.a.n_kv) kvh = 0;
+        }
+      }
+    }
     if constexpr (!SPARSE) {  // earlier rows end earlier than the sequence
       const int own = max(1, (s.t1 + kTile - 1) / kTile);
       s.lo = min(s.lo, own);
@@ -255,30 +276,36 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int per = 32 / p.ppt;  // tiles whose pages one load of the warp covers
     int it = 0;
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const int n_list = SPARSE ? p.n_sel : (s.t1 + p.page - 1) / p.page;
-      const int n_vis = (s.t1 + p.page - 1) / p.page;
-      const int32_t* list = SPARSE ? p.sel + (static_cast<int64_t>(s.row0) * p.a.n_kv + s.kvh) * p.n_sel : nullptr;
-      const auto fetch = [&](int tile0, int& j, int& pg, float& ks, float& vs) {
-        const int l = tile0 * p.ppt + lane;
-        j = -1;
-        if (l < n_list) j = SPARSE ? __ldg(list + l) : l;
-        pg = j >= 0 && j < n_vis ? paged_page(p.a, s.b, j) : -1;
-        ks = vs = 0.f;
-        if (F8 && pg >= 0) {
-          const int64_t u = static_cast<int64_t>(pg) * p.a.n_kv + s.kvh;
-          ks = __ldg(p.a.k_scale + u);
-          vs = __ldg(p.a.v_scale + u);
-        }
-      };
-      int j, pg, jn, pn;
-      float ks, vs, kn, vn;
-      fetch(s.lo, jn, pn, kn, vn);
+    // list entry, pool page and scales of the lane's page in a batch of tiles
+    const auto fetch = [&](const Seg& g, int tile0, int& j, int& pg, float& ks, float& vs) {
+      const int n_vis = (g.t1 + p.page - 1) >> p.shift, n_list = SPARSE ? p.n_sel : n_vis;
+      const int l = tile0 * p.ppt + lane;
+      j = -1;
+      if (l < n_list) j = SPARSE ? __ldg(p.sel + (static_cast<int64_t>(g.row0) * p.a.n_kv + g.kvh) * p.n_sel + l) : l;
+      pg = j >= 0 && j < n_vis ? paged_page(p.a, g.b, j) : -1;
+      ks = vs = 0.f;
+      if (F8 && pg >= 0) {
+        const int64_t u = static_cast<int64_t>(pg) * p.a.n_kv + g.kvh;
+        ks = __ldg(p.a.k_scale + u);
+        vs = __ldg(p.a.v_scale + u);
+      }
+    };
+    int j, pg, jn, pn, j2, p2;
+    float ks, vs, kn, vn, k2, v2;
+    Seg s2;
+    bool more = walk.next(s2);
+    if (more) fetch(s2, s2.lo, j2, p2, k2, v2);
+    while (ok && more) {
+      s = s2;
+      jn = j2; pn = p2; kn = k2; vn = v2;
+      // the next unit's first pages, while this one's tiles are loaded
+      more = walk.next(s2);
+      if (more) fetch(s2, s2.lo, j2, p2, k2, v2);
       for (int i = s.lo; i < s.hi; ++i, ++it) {
         const int in = (i - s.lo) % per;
         if (in == 0) {
           j = jn; pg = pn; ks = kn; vs = vn;
-          if (i + per < s.hi) fetch(i + per, jn, pn, kn, vn);
+          if (i + per < s.hi) fetch(s, i + per, jn, pn, kn, vn);
         }
         const int src = in * p.ppt + lane % p.ppt;
         const int mj = __shfl_sync(0xffffffffu, j, src), mp = __shfl_sync(0xffffffffu, pg, src);
@@ -378,20 +405,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     int it = 0, seg = 0;
     bool ok = true;
 
-    // Q rows of a segment as the MMA's B operand (8 columns per thread)
-    const auto load_q = [&](const Seg& g, int par) {
-      constexpr int kVecs = D / 8, kStep = C::kEpiWarps * 32 / kVecs;
-      const int vec = threadIdx.x % kVecs;
+    // Q rows of a segment as the MMA's B operand, 8 columns per thread: loaded
+    // while the segment before is worked on, laid out when its QK are complete
+    constexpr int kVecs = D / 8, kStep = C::kEpiWarps * 32 / kVecs, kQSteps = (NH + kStep - 1) / kStep;
+    const int vec = threadIdx.x % kVecs;
+    uint4 qw[kQSteps];
+    const auto fetch_q = [&](const Seg& g) {
       const int heads = min(p.Gx, p.G - g.h0);
 #pragma unroll
-      for (int n0 = 0; n0 < NH; n0 += kStep) {
-        const int n = n0 + threadIdx.x / kVecs;
-        uint4 w = make_uint4(0, 0, 0, 0);
+      for (int e = 0; e < kQSteps; ++e) {
+        const int n = e * kStep + threadIdx.x / kVecs;
+        qw[e] = make_uint4(0, 0, 0, 0);
         if (n < g.nh) {
-          const int r = n / heads;
-          w = __ldg(reinterpret_cast<const uint4*>(
+          const int r = SPARSE ? 0 : n / heads;
+          qw[e] = __ldg(reinterpret_cast<const uint4*>(
               p.q + (static_cast<int64_t>(g.row0 + r) * p.n_h + g.kvh * p.G + g.h0 + (n - r * heads)) * D + vec * 8));
         }
+      }
+    };
+    const auto store_q = [&](int par) {
+#pragma unroll
+      for (int e = 0; e < kQSteps; ++e) {
+        const int n = e * kStep + threadIdx.x / kVecs;
+        const uint4 w = qw[e];
         if constexpr (F8) {
           float f[8], amax = 0.f;
           bf16x8_to_f32(w, f);
@@ -429,27 +465,34 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     };
 
     bool more = walk.next(s);
-    if (more) load_q(s, 0);
-    else if (p.part_l && threadIdx.x < NH) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;  // no part of any unit
+    if (more) {
+      fetch_q(s);
+      store_q(0);
+    } else if (p.part_l && threadIdx.x < NH) {
+      p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;  // no part of any unit
+    }
     while (ok && more) {
+      const Seg cur = s;
+      more = walk.next(s);
+      if (more) fetch_q(s);
       // lane h (mod HG) keeps the reference exponents of head h: m of the
       // weights, mp of the weighted V scales; every thread its keys' sums
       float m = -INFINITY, mp = -INFINITY, l[HG];
 #pragma unroll
       for (int h = 0; h < HG; ++h) l[h] = 0.f;
-      const int heads = min(p.Gx, p.G - s.h0);
+      const int heads = min(p.Gx, p.G - cur.h0);
       float c[HG];  // factors of the scores
       if constexpr (F8) {
         ok = mbar_wait(q_full, seg & 1, abort_flag);
 #pragma unroll
         for (int h = 0; h < HG; ++h) c[h] = cq[(seg & 1) * NH + gh + h];
       }
-      for (int i = s.lo; i < s.hi; ++i, ++it) {
+      for (int i = cur.lo; i < cur.hi; ++i, ++it) {
         const int buf = it & 1;
         ok = mbar_wait(&meta_full[it % kMetas], (it / kMetas) & 1, abort_flag) && ok;
         const int4 mt = ok ? meta[it % kMetas * 8 + (key >> p.shift)] : make_int4(kNoPage, 0, 0, 0);
         const float ks = __int_as_float(mt.y), vs = __int_as_float(mt.z);
-        const int pos = mt.x + (key & (p.page - 1)), past = pos - s.t0;
+        const int pos = mt.x + (key & (p.page - 1)), past = pos - cur.t0;
         float x[HG];
         float lvs = 0.f;
         if constexpr (F8) lvs = __log2f(warp_max_f32(vs));
@@ -474,7 +517,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const bool edge = __any_sync(0xffffffffu, past >= 0);
         if (edge) {
           // head row n sees this key from n = nmin on (rows see one position more each)
-          const int nmin = past < 0 ? 0 : (past < s.nr ? (past + 1) * heads : kNoPage);
+          const int nmin = past < 0 ? 0 : (past < cur.nr ? (past + 1) * heads : kNoPage);
 #pragma unroll
           for (int h = 0; h < HG; ++h) x[h] = gh + h >= nmin ? x[h] : -INFINITY;
         }
@@ -557,7 +600,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
         }
         // ---- O follows a new reference exponent
-        if (grew && i > s.lo) {  // the same for the whole group
+        if (grew && i > cur.lo) {  // the same for the whole group
           ok = mbar_wait(&pv_done[buf ^ 1], ((it - 1) >> 1) & 1, abort_flag) && ok;
           ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
@@ -590,7 +633,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               for (int v = 0; v < C::kRowB / 16; ++v) {
                 uint4 w = row[v];
                 uint32_t y[4] = {w.x, w.y, w.z, w.w};
-                bool bad = pos >= s.t1;
+                bool bad = pos >= cur.t1;
                 if (!bad) {
 #pragma unroll
                   for (int u = 0; u < 4; ++u) {
@@ -613,10 +656,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
       // ---- the next segment's queries: every QK of this one is complete
-      Seg cur = s;
       const int last = it - 1;
-      more = ok && walk.next(s);
-      if (more) load_q(s, (seg + 1) & 1);
+      if (more) store_q((seg + 1) & 1);
 
       // ---- output of the segment
 #pragma unroll
@@ -649,18 +690,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int h = 0; h < HG; ++h) o[h] = any ? __uint_as_float(a[h]) : 0.f;
       }
       tc_fence_before();
-      if (lane < HG) {  // head h: the reference of its sum, and what turns O into weights of that reference
-        bc[lane] = m == -INFINITY ? 0.f : m;
-        bc[HG + lane] = F8 ? ex2_approx((mp == -INFINITY ? 0.f : mp) - (m == -INFINITY ? 0.f : m) - 8.f) : 1.f;
+      // lane h: total, 1 / total and log2 of head h
+      {
+        const float* t = lsum + gh + lane % HG;
+        const float sum = (t[0] + t[NH]) + (t[2 * NH] + t[3 * NH]);
+        const float ml = m == -INFINITY ? 0.f : m, mv = mp == -INFINITY ? 0.f : mp;
+        const float f = F8 ? ex2_approx(mv - ml - 8.f) : 1.f;
+        const float l2 = sum == 0.f ? -INFINITY : ml + log2f(sum);
+        if (lane < HG) bc[lane] = sum == 0.f ? 0.f : f / sum;
+        if (wq == 0 && lane < HG && gh + lane < cur.nh) {
+          const int n = gh + lane, r = SPARSE ? 0 : n / heads;
+          if (cur.slot < 0) {
+            if (p.lse) p.lse[static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads)] = sum == 0.f ? -INFINITY : l2 * kLn2;
+          } else {
+            p.part_l[(2ll * blockIdx.x + cur.slot) * NH + n] = l2;
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
 #pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        const float* t = lsum + gh + h;
-        l[h] = (t[0] + t[NH]) + (t[2 * NH] + t[3 * NH]);
-        const float f = bc[HG + h];
-        o[h] = l[h] == 0.f ? 0.f : o[h] * f / l[h];
-      }
+      for (int h = 0; h < HG; ++h) o[h] = bc[h] == 0.f ? 0.f : o[h] * bc[h];
       if (poison[seg & 1] && key < D) {  // values that are not finite, for the rows that see them
         for (int t = max(cur.t0, cur.lo * kTile); t < min(cur.t1, cur.hi * kTile); ++t) {
           const int pg = paged_page(p.a, cur.b, t / p.page);
@@ -675,28 +724,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if ((gh + h) / heads > t - cur.t0) o[h] += v;
         }
       }
-      if (cur.slot < 0) {
-        if (key < D) {
+      if (key < D) {
+        if (cur.slot < 0) {
+          int r = SPARSE ? 0 : gh / heads, g = gh - r * heads;
+          dsa_bf16* dst = p.out + (static_cast<int64_t>(cur.row0) * p.n_h + cur.kvh * p.G + cur.h0) * D + key;
 #pragma unroll
           for (int h = 0; h < HG; ++h) {
-            const int n = gh + h;
-            if (n < cur.nh) {
-              const int r = n / heads;
-              const int64_t at = static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads);
-              const __nv_bfloat16 y = __float2bfloat16_rn(o[h]);
-              p.out[at * D + key] = *reinterpret_cast<const dsa_bf16*>(&y);
-              if (key == 0 && p.lse) p.lse[at] = l[h] == 0.f ? -INFINITY : (bc[h] + log2f(l[h])) * kLn2;
-            }
+            const __nv_bfloat16 y = __float2bfloat16_rn(o[h]);
+            if (gh + h < cur.nh) dst[(r * p.n_h + g) * D] = *reinterpret_cast<const dsa_bf16*>(&y);
+            if (++g == heads) { g = 0; ++r; }
           }
-        }
-      } else {
-        const int64_t slot = 2 * blockIdx.x + cur.slot;
-        if (key < D) {
+        } else {
+          float* dst = p.part_o + ((2ll * blockIdx.x + cur.slot) * NH + gh) * D + key;
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            p.part_o[(slot * NH + gh + h) * D + key] = o[h];
-            if (key == 0) p.part_l[slot * NH + gh + h] = l[h] == 0.f ? -INFINITY : bc[h] + log2f(l[h]);
-          }
+          for (int h = 0; h < HG; ++h) dst[h * D] = o[h];
         }
       }
       if (threadIdx.x == 0 && cur.slot != 0 && p.meta) p.meta[cur.unit] = cur.slot < 0 ? make_int2(-1, -1) : make_int2(blockIdx.x, cur.last_cta);
