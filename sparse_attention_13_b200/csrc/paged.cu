@@ -66,7 +66,8 @@ struct AppendParams {
   const float *cos, *sin;
   int n_h, half, interleaved, n_pos;
   int touched;     // pages a sequence can touch
-  int64_t units;   // blocks of cache pages; the blocks after them rotate q
+  int64_t units;   // blocks of cache pages: every period-th; the others rotate q
+  int period;
   int q_runs, q_heads;  // runs of heads a row is cut into, heads of a run
 };
 
@@ -134,7 +135,7 @@ __device__ __forceinline__ float block_max(float x, float* red) {
 // 8 columns of every (256 / (D/8))-th slot, in registers from the load to the
 // store.  Bound by memory: new rows in, cache rows out, each once.
 template <int D, int PAGE, bool F8>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;                    // threads per slot
   constexpr int kRows = kAppendThreads / kVecs;   // slots per step
   constexpr int kSteps = PAGE > kRows ? PAGE / kRows : 1;
@@ -144,10 +145,14 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   pdl_wait();
   const int vec = threadIdx.x % kVecs, g = threadIdx.x / kVecs, c = vec * 8;
 
-  if (blockIdx.x >= p.units) {  // queries: a warp per row and run of heads
+  // cache blocks (long chains of latencies) are spread among the query blocks
+  // (streams), so that both kinds share every SM
+  const int64_t turn_of = blockIdx.x / p.period;
+  const bool cache = blockIdx.x % p.period == 0 && turn_of < p.units;
+  if (!cache) {  // queries: a warp per row and run of heads
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes;  // lanes per head (two vectors each), heads per step
     const int lane = threadIdx.x & 31;
-    const int64_t w = (blockIdx.x - p.units) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int64_t w = (blockIdx.x - min(p.units, turn_of + 1)) * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int64_t row = w / p.q_runs;
     if (row >= p.a.total_q) return;
     const int b = paged_seq(p.a, static_cast<int>(row));
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     return;
   }
 
-  int u = static_cast<int>(blockIdx.x);
+  int u = static_cast<int>(turn_of);
   const bool is_v = u & 1;
   u >>= 1;
   const int head = u % p.a.n_kv;
@@ -366,7 +371,7 @@ constexpr int kSelMaxPages = 49152;  // one f32 key per visible page in shared m
 struct SelParams {
   PagedArgs a;
   const dsa_bf16* q;
-  int n_h, page, inclusive, n_sel, n_first, n_last;
+  int n_h, page, shift, inclusive, n_sel, n_first, n_last;
   int ranks;                   // blocks of a decode row's cluster
   int row_blocks, key_stride;  // many rows: blocks of a sequence, keys of a row
   int32_t* sel;
@@ -406,16 +411,6 @@ __device__ __forceinline__ void pooled_query(const SelParams& p, int64_t row, in
   for (int i = 0; i < kCols; ++i) qc[lane * kCols + i] = fine ? static_cast<int8_t>(__float2int_rn(__fmul_rn(f[i], inv))) : 0;
 }
 
-template <int D>
-__device__ __forceinline__ int dot_codes(const int4 (&s)[D / 16], const int8_t* qc) {
-  int dot = 0;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const int4 x = *reinterpret_cast<const int4*>(qc + 16 * i);
-    dot = __dp4a(s[i].x, x.x, __dp4a(s[i].y, x.y, __dp4a(s[i].z, x.z, __dp4a(s[i].w, x.w, dot))));
-  }
-  return dot;
-}
 template <int D>
 __device__ __forceinline__ void load_summary(const PagedArgs& a, int64_t unit, int4 (&s)[D / 16], float& scale) {
 #pragma unroll
@@ -646,13 +641,13 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
 }
 
 // Many rows: one block per (eight rows of a sequence, head).  A page's summary
-// is read once for the eight rows; then a warp selects for each row, its keys
-// in registers (up to 1,024 pages) or in shared memory.
-constexpr int kSelRows = 8;
+// is read once for the eight rows; then a warp selects for each row as above.
+constexpr int kSelRows = 8, kRowBins = 256;
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelParams p) {
   extern __shared__ __align__(16) uint32_t keys[];  // [kSelRows][p.key_stride]
   __shared__ __align__(16) int8_t qc[kSelRows][D];
+  __shared__ int hist[kSelRows][kRowBins];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -671,17 +666,35 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
     if (warp < nr) pooled_query<D>(p, r0 + first + warp, head, qc[warp]);
     __syncthreads();
     const int tail = p.page, t0 = paged_visible(p.a, b, first, p.inclusive);
-#pragma unroll 2
-    for (int j = tid; j < n_max; j += kSelThreads) {
-      const int pg = paged_page(p.a, b, j);
-      int4 s[D / 16];
-      float scale = 0.f;
-      if (pg >= 0) load_summary<D>(p.a, static_cast<int64_t>(pg) * p.a.n_kv + head, s, scale);
+    for (int j = tid; j < n_max; j += 2 * kSelThreads) {  // two pages share a row's codes
+      int pg[2];
+      int4 s[2][D / 16];
+      float scale[2] = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) pg[e] = j + e * kSelThreads < n_max ? paged_page(p.a, b, j + e * kSelThreads) : -1;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (pg[e] >= 0) load_summary<D>(p.a, static_cast<int64_t>(pg[e]) * p.a.n_kv + head, s[e], scale[e]);
+        else {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) s[e][i] = make_int4(0, 0, 0, 0);
+        }
       for (int r = 0; r < nr; ++r) {
-        const int nn = (min(t0 + r, p.a.max_Lk) + tail - 1) / tail;
-        uint32_t key = kForced;
-        if (j >= p.n_first && j < nn - p.n_last) key = pg >= 0 ? float_key(__fmul_rn(static_cast<float>(dot_codes<D>(s, qc[r])), scale)) : 0u;
-        keys[r * p.key_stride + j] = key;
+        const int nn = (min(t0 + r, p.a.max_Lk) + tail - 1) >> p.shift;
+        int dot[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int4 x = *reinterpret_cast<const int4*>(&qc[r][16 * i]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            dot[e] = __dp4a(s[e][i].x, x.x, __dp4a(s[e][i].y, x.y, __dp4a(s[e][i].z, x.z, __dp4a(s[e][i].w, x.w, dot[e]))));
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int je = j + e * kSelThreads;
+          const bool scored = je >= p.n_first && je < nn - p.n_last;
+          if (je < n_max) keys[r * p.key_stride + je] = scored ? float_key(__fmul_rn(static_cast<float>(dot[e]), scale[e])) : kForced;
+        }
       }
     }
     __syncthreads();
@@ -693,37 +706,87 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
     return;
   }
   const uint32_t* kr = keys + warp * p.key_stride;
-  constexpr int kRegs = 32;
-  const bool in_regs = n <= 32 * kRegs;
-  uint32_t k[kRegs];
+  const unsigned lt = (1u << lane) - 1u;
   uint32_t low = kForced, hi = 0u;
-  if (in_regs) {
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i) {
-      k[i] = i * 32 + lane < n ? kr[i * 32 + lane] : 0u;
-      if (i * 32 + lane < n) low = min(low, k[i]);
-      if (k[i] != kForced) hi = max(hi, k[i]);
-    }
-  } else {
-    for (int j = lane; j < n; j += 32) {
-      low = min(low, kr[j]);
-      if (kr[j] != kForced) hi = max(hi, kr[j]);
-    }
+  for (int j = lane; j < n; j += 32) {
+    const uint32_t x = kr[j];
+    low = min(low, x);
+    if (x != kForced) hi = max(hi, x);
   }
   low = __reduce_min_sync(0xffffffffu, low);
-  hi = __reduce_max_sync(0xffffffffu, hi) + 1u;
+  hi = __reduce_max_sync(0xffffffffu, hi);
   int above = p.n_first + p.n_last;
-  bool exact = false;
-  if (above >= p.n_sel) { low = kForced; exact = true; }
+  bool exact = above >= p.n_sel;
+  const float v0 = key_value(low), gain = kRowBins / (key_value(hi) - v0);
+  const bool spread = hi > low && gain < 1e30f;
+  if (exact) low = kForced;
+  hi += 1u;
+  if (!exact && spread) {
+    // equal steps of value: the step that holds the n_sel-th largest key, and
+    // its keys (up to 32) ranked against each other
+    int* h = hist[warp];
+    const auto bin = [&](uint32_t key) { return min(kRowBins - 1, static_cast<int>((key_value(key) - v0) * gain)); };  // grows with the value
+#pragma unroll
+    for (int i = 0; i < kRowBins / 32; ++i) h[i * 32 + lane] = 0;
+    __syncwarp();
+#pragma unroll 4
+    for (int j = lane; j < n; j += 32) {
+      const uint32_t x = kr[j];
+      if (x != kForced) atomicAdd(&h[bin(x)], 1);
+    }
+    __syncwarp();
+    constexpr int kPer = kRowBins / 32;  // lane 0 holds the highest steps
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) { c[i] = h[kRowBins - 1 - (lane * kPer + i)]; sum += c[i]; }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, above + incl >= p.n_sel)) - 1;
+    int run = above + incl - sum, pick = 0, in_bin = 0;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (!found && run + c[i] >= p.n_sel) { found = true; pick = kRowBins - 1 - (lane * kPer + i); in_bin = c[i]; }
+      if (!found) run += c[i];
+    }
+    pick = __shfl_sync(0xffffffffu, pick, src);
+    in_bin = __shfl_sync(0xffffffffu, in_bin, src);
+    run = __shfl_sync(0xffffffffu, run, src);
+    if (in_bin <= 32) {
+      int got = 0;
+      __syncwarp();
+#pragma unroll 2
+      for (int j0 = 0; j0 < n; j0 += 32) {
+        const uint32_t x = j0 + lane < n ? kr[j0 + lane] : kForced;
+        const bool in = x != kForced && bin(x) == pick;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (in) h[got + __popc(m & lt)] = static_cast<int>(x);
+        got += __popc(m);
+      }
+      __syncwarp();
+      const uint32_t mine = lane < in_bin ? static_cast<uint32_t>(h[lane]) : 0u;
+      int gt = 0, ge = 0;
+      for (int i = 0; i < in_bin; ++i) {
+        const uint32_t x = static_cast<uint32_t>(h[i]);
+        gt += x > mine;
+        ge += x >= mine;
+      }
+      const bool is = lane < in_bin && run + gt < p.n_sel && run + ge >= p.n_sel;
+      const int who = __ffs(__ballot_sync(0xffffffffu, is)) - 1;
+      low = __shfl_sync(0xffffffffu, mine, who);
+      above = run + __shfl_sync(0xffffffffu, gt, who);
+      exact = run + __shfl_sync(0xffffffffu, ge, who) == p.n_sel;
+      hi = low + 1u;
+    }
+  }
   for (int step = 0; !exact && hi - low > 1u; ++step) {
     const uint32_t mid = key_between(low, hi, step);
     int c = 0;
-    if (in_regs) {
-#pragma unroll
-      for (int i = 0; i < kRegs; ++i) c += k[i] >= mid;
-    } else {
-      for (int j = lane; j < n; j += 32) c += kr[j] >= mid;
-    }
+    for (int j = lane; j < n; j += 32) c += kr[j] >= mid;
     c = __reduce_add_sync(0xffffffffu, c);
     if (c >= p.n_sel) {
       low = mid;
@@ -735,12 +798,13 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
   }
   const int want = exact ? p.n_sel : p.n_sel - above;
   int at = 0, ties = 0;
-  const unsigned lt = (1u << lane) - 1u;
-  for (int j0 = 0; j0 < n && at + min(ties, want) < p.n_sel; j0 += 32) {
+#pragma unroll 2
+  for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
     const uint32_t key = j < n ? kr[j] : 0u;
     const bool gt = j < n && (exact ? key >= low : key > low), eq = j < n && !exact && key == low;
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    if (!(bg | be)) continue;
     const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
     if (gt) out[g0 + min(e0, want)] = j;
     else if (eq && e0 < want) out[g0 + e0] = j;
@@ -792,6 +856,7 @@ dsa_status dsa_paged_append(const dsa_paged_kv* kv, const dsa_paged_batch* batch
   p.q_runs = q ? (n_h + p.q_heads - 1) / p.q_heads : 1;
   const int64_t q_blocks = q ? (static_cast<int64_t>(batch->total_q) * p.q_runs + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : 0;
   const int64_t grid = p.units + q_blocks;
+  p.period = static_cast<int>(std::min<int64_t>(1 << 20, grid / p.units));
   if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: batch too large");
   const cudaError_t e = kv->D == 64
       ? launch_append<64>(p, kv->page, kv->fmt == DSA_KV_E4M3, static_cast<unsigned>(grid), static_cast<cudaStream_t>(stream))
@@ -815,7 +880,7 @@ dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, con
   const int max_n = (batch->max_Lk + kv->page - 1) / kv->page;
   if (n_sel > 1024 || max_n > kSelMaxPages)
     return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: n_sel <= 1024 and at most 49152 pages per sequence");
-  p.q = q; p.n_h = n_h; p.page = kv->page; p.inclusive = inclusive; p.n_sel = n_sel; p.n_first = n_first; p.n_last = n_last;
+  p.q = q; p.n_h = n_h; p.page = kv->page; p.shift = kv->page == 16 ? 4 : kv->page == 32 ? 5 : kv->page == 64 ? 6 : 7; p.inclusive = inclusive; p.n_sel = n_sel; p.n_first = n_first; p.n_last = n_last;
   p.sel = sel;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool d64 = kv->D == 64;

@@ -748,7 +748,7 @@ def paged_append(kv: PagedKV, batch: PagedBatch, k, v, cos=None, sin=None, *, q=
         n_h = q.shape[1]
         qs, pq = _token_rows(q, dev, "q", rows, n_h, D), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((rows, n_h, D), dtype=torch.bfloat16, device=q.device)
+            q_out = q.new_empty((rows, n_h, D))
         po = _dense(q_out, torch.bfloat16, (rows, n_h, D), dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
@@ -781,7 +781,7 @@ def page_topk(q, kv: PagedKV, batch: PagedBatch, n_sel: int, *, n_first: int = 1
     n_h = _queries(q, rows, D)
     pq = _dense(q, torch.bfloat16, (rows, n_h, D), dev, "q")
     if out is None:
-        out = torch.empty((rows, d.n_kv, n_sel), dtype=torch.int32, device=q.device)
+        out = q.new_empty((rows, d.n_kv, n_sel), dtype=torch.int32)
     po = _dense(out, torch.int32, (rows, d.n_kv, n_sel), dev, "out")
     _on_cache(batch, dev)
     with _on(dev) as stream:
@@ -809,7 +809,7 @@ def paged_attn(q, kv: PagedKV, batch: PagedBatch, scale: float, *, sel=None, inc
         n_sel = sel.shape[-1]
         psel = _dense(sel, torch.int32, (rows, d.n_kv, n_sel), dev, "sel")
     if out is None:
-        out = torch.empty((rows, n_h, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q)
     po = _dense(out, torch.bfloat16, (rows, n_h, D), dev, "out")
     if lse is not None:
         pl = _dense(lse, torch.float32, (rows, n_h), dev, "lse")
@@ -817,8 +817,7 @@ def paged_attn(q, kv: PagedKV, batch: PagedBatch, scale: float, *, sel=None, inc
     with _on(dev) as stream:
         L = lib()
         if ws is None:
-            ws = torch.empty(max(L.dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel), 16), dtype=torch.uint8,
-                             device=q.device)
+            ws = q.new_empty(max(L.dsa_paged_attn_workspace(kv.ref, batch.ref, n_h, n_sel), 16), dtype=torch.uint8)
         elif not ws.is_contiguous() or ws.get_device() != dev:
             raise ValueError(f"ws must be contiguous on cuda:{dev}")
         _check(L.dsa_paged_attn(pq, n_h, kv.ref, batch.ref, int(inclusive), psel, n_sel, scale, po, pl, ws.data_ptr(),
