@@ -640,12 +640,23 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
   }
 }
 
-// Many rows: one block per (eight rows of a sequence, head).  A page's summary
-// is read once for the eight rows; then a warp selects for each row as above.
+// D += A B^T for 16 x 32 and 8 x 32 signed bytes, whole numbers throughout.
+__device__ __forceinline__ void mma_s8_16x8x32(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Many rows: one block per (eight rows of a sequence, head).  The scores of
+// eight rows and sixteen pages are one small integer matrix product, with the
+// columns permuted so that a lane's operands are 16 consecutive bytes; then a
+// warp selects for each row from the scores in shared memory (forced pages:
+// +inf).  Bound by instruction issue: about 1,700 per warp and row at 1,000
+// pages, a third of them the scores.
 constexpr int kSelRows = 8, kRowBins = 256;
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelParams p) {
-  extern __shared__ __align__(16) uint32_t keys[];  // [kSelRows][p.key_stride]
+  extern __shared__ __align__(16) float score[];  // [kSelRows][p.key_stride]
   __shared__ __align__(16) int8_t qc[kSelRows][D];
   __shared__ int hist[kSelRows][kRowBins];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -659,42 +670,43 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
   const int first = rest % p.row_blocks * kSelRows;
   const int nr = min(kSelRows, rows - first);
   if (nr <= 0) return;
-  const auto pages_of = [&](int r) { return (paged_visible(p.a, b, first + r, p.inclusive) + p.page - 1) / p.page; };
+  const auto pages_of = [&](int r) { return (paged_visible(p.a, b, first + r, p.inclusive) + p.page - 1) >> p.shift; };
   const int n_max = pages_of(nr - 1);
   const int n = warp < nr ? pages_of(warp) : 0;
   if (n_max > p.n_sel) {
     if (warp < nr) pooled_query<D>(p, r0 + first + warp, head, qc[warp]);
     __syncthreads();
-    const int tail = p.page, t0 = paged_visible(p.a, b, first, p.inclusive);
-    for (int j = tid; j < n_max; j += 2 * kSelThreads) {  // two pages share a row's codes
-      int pg[2];
-      int4 s[2][D / 16];
-      float scale[2] = {0.f, 0.f};
+    constexpr int kVecs = D / 64;  // 16-byte vectors of a lane, for a page or a row
+    const int g = lane >> 2, tq = lane & 3;
+    int4 q[kVecs];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) pg[e] = j + e * kSelThreads < n_max ? paged_page(p.a, b, j + e * kSelThreads) : -1;
+    for (int v = 0; v < kVecs; ++v) q[v] = *reinterpret_cast<const int4*>(&qc[g][v * 64 + tq * 16]);
+    int last[2];  // pages before the forced ones, of the lane's two rows
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (pg[e] >= 0) load_summary<D>(p.a, static_cast<int64_t>(pg[e]) * p.a.n_kv + head, s[e], scale[e]);
-        else {
+    for (int c = 0; c < 2; ++c) last[c] = pages_of(min(2 * tq + c, nr - 1)) - p.n_last;
+#pragma unroll 2
+    for (int j0 = warp * 16; j0 < n_max; j0 += 16 * (kSelThreads / 32)) {
+      int4 s[2][kVecs];
+      float scale[2];
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) s[e][i] = make_int4(0, 0, 0, 0);
-        }
-      for (int r = 0; r < nr; ++r) {
-        const int nn = (min(t0 + r, p.a.max_Lk) + tail - 1) >> p.shift;
-        int dot[2] = {0, 0};
+      for (int e = 0; e < 2; ++e) {
+        const int j = j0 + g + 8 * e, pg = j < n_max ? paged_page(p.a, b, j) : -1;
+        const int64_t unit = static_cast<int64_t>(max(pg, 0)) * p.a.n_kv + head;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int4 x = *reinterpret_cast<const int4*>(&qc[r][16 * i]);
+        for (int v = 0; v < kVecs; ++v) s[e][v] = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D + v * 64) + tq);
+        scale[e] = pg >= 0 ? __ldg(p.a.sum_scale + unit) : 0.f;
+      }
+      int d[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            dot[e] = __dp4a(s[e][i].x, x.x, __dp4a(s[e][i].y, x.y, __dp4a(s[e][i].z, x.z, __dp4a(s[e][i].w, x.w, dot[e]))));
-        }
+      for (int v = 0; v < kVecs; ++v) {
+        mma_s8_16x8x32(d, s[0][v].x, s[1][v].x, s[0][v].y, s[1][v].y, q[v].x, q[v].y);
+        mma_s8_16x8x32(d, s[0][v].z, s[1][v].z, s[0][v].w, s[1][v].w, q[v].z, q[v].w);
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int je = j + e * kSelThreads;
-          const bool scored = je >= p.n_first && je < nn - p.n_last;
-          if (je < n_max) keys[r * p.key_stride + je] = scored ? float_key(__fmul_rn(static_cast<float>(dot[e]), scale[e])) : kForced;
-        }
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + g + 8 * (e >> 1), c = e & 1;
+        const float x = __fmul_rn(static_cast<float>(d[e]), scale[e >> 1]);
+        if (j < n_max) score[(2 * tq + c) * p.key_stride + j] = j >= p.n_first && j < last[c] ? x : INFINITY;
       }
     }
     __syncthreads();
@@ -705,35 +717,35 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
     for (int e = lane; e < p.n_sel; e += 32) out[e] = e < n ? e : -1;
     return;
   }
-  const uint32_t* kr = keys + warp * p.key_stride;
+  const float* kr = score + warp * p.key_stride;
   const unsigned lt = (1u << lane) - 1u;
-  uint32_t low = kForced, hi = 0u;
+  float v_lo = INFINITY, v_hi = -INFINITY;  // of the finite scores
   for (int j = lane; j < n; j += 32) {
-    const uint32_t x = kr[j];
-    low = min(low, x);
-    if (x != kForced) hi = max(hi, x);
+    const float x = kr[j];
+    v_lo = fminf(v_lo, x);
+    if (x < INFINITY) v_hi = fmaxf(v_hi, x);
   }
-  low = __reduce_min_sync(0xffffffffu, low);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  int above = p.n_first + p.n_last;
-  bool exact = above >= p.n_sel;
-  const float v0 = key_value(low), gain = kRowBins / (key_value(hi) - v0);
-  const bool spread = hi > low && gain < 1e30f;
-  if (exact) low = kForced;
-  hi += 1u;
-  if (!exact && spread) {
-    // equal steps of value: the step that holds the n_sel-th largest key, and
-    // its keys (up to 32) ranked against each other
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    v_lo = fminf(v_lo, __shfl_xor_sync(0xffffffffu, v_lo, o));
+    v_hi = fmaxf(v_hi, __shfl_xor_sync(0xffffffffu, v_hi, o));
+  }
+  // thr: the n_sel-th largest score; `above` scores are larger, and `want` of
+  // those equal to it are taken (all of them when exact)
+  float thr = INFINITY;
+  int above = 0, forced = p.n_first + p.n_last;
+  bool done = forced >= p.n_sel, exact = done;
+  const float gain = kRowBins / (v_hi - v_lo), off = -v_lo * gain;
+  if (!done && v_hi > v_lo && gain < 1e30f && fabsf(off) < 1e30f) {
+    // equal steps of value (forced pages in the last one): the step that holds
+    // the n_sel-th largest score, and its scores (up to 32) ranked
     int* h = hist[warp];
-    const auto bin = [&](uint32_t key) { return min(kRowBins - 1, static_cast<int>((key_value(key) - v0) * gain)); };  // grows with the value
+    const auto bin = [&](float x) { return min(kRowBins - 1, static_cast<int>(fmaf(x, gain, off))); };  // grows with the value
 #pragma unroll
     for (int i = 0; i < kRowBins / 32; ++i) h[i * 32 + lane] = 0;
     __syncwarp();
 #pragma unroll 4
-    for (int j = lane; j < n; j += 32) {
-      const uint32_t x = kr[j];
-      if (x != kForced) atomicAdd(&h[bin(x)], 1);
-    }
+    for (int j = lane; j < n; j += 32) atomicAdd(&h[max(0, bin(kr[j]))], 1);
     __syncwarp();
     constexpr int kPer = kRowBins / 32;  // lane 0 holds the highest steps
     int c[kPer], sum = 0;
@@ -745,8 +757,8 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, above + incl >= p.n_sel)) - 1;
-    int run = above + incl - sum, pick = 0, in_bin = 0;
+    const int src = __ffs(__ballot_sync(0xffffffffu, incl >= p.n_sel)) - 1;
+    int run = incl - sum, pick = 0, in_bin = 0;
     bool found = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -759,57 +771,86 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
     if (in_bin <= 32) {
       int got = 0;
       __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
       for (int j0 = 0; j0 < n; j0 += 32) {
-        const uint32_t x = j0 + lane < n ? kr[j0 + lane] : kForced;
-        const bool in = x != kForced && bin(x) == pick;
+        const float x = j0 + lane < n ? kr[j0 + lane] : 0.f;
+        const bool in = j0 + lane < n && max(0, bin(x)) == pick;
         const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (in) h[got + __popc(m & lt)] = static_cast<int>(x);
-        got += __popc(m);
+        if (m) {
+          if (in) h[got + __popc(m & lt)] = __float_as_int(x);
+          got += __popc(m);
+        }
       }
       __syncwarp();
-      const uint32_t mine = lane < in_bin ? static_cast<uint32_t>(h[lane]) : 0u;
+      const float mine = lane < in_bin ? __int_as_float(h[lane]) : 0.f;
       int gt = 0, ge = 0;
       for (int i = 0; i < in_bin; ++i) {
-        const uint32_t x = static_cast<uint32_t>(h[i]);
+        const float x = __int_as_float(h[i]);
         gt += x > mine;
         ge += x >= mine;
       }
       const bool is = lane < in_bin && run + gt < p.n_sel && run + ge >= p.n_sel;
       const int who = __ffs(__ballot_sync(0xffffffffu, is)) - 1;
-      low = __shfl_sync(0xffffffffu, mine, who);
+      thr = __shfl_sync(0xffffffffu, mine, who);
       above = run + __shfl_sync(0xffffffffu, gt, who);
       exact = run + __shfl_sync(0xffffffffu, ge, who) == p.n_sel;
-      hi = low + 1u;
+      done = true;
     }
   }
-  for (int step = 0; !exact && hi - low > 1u; ++step) {
-    const uint32_t mid = key_between(low, hi, step);
-    int c = 0;
-    for (int j = lane; j < n; j += 32) c += kr[j] >= mid;
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (c >= p.n_sel) {
-      low = mid;
-      exact = c == p.n_sel;
-    } else {
-      hi = mid;
-      above = c;
+  if (!done) {  // halving: fewer than n_sel scores are >= hi's, at least n_sel >= lo's
+    uint32_t lo = float_key(v_lo), hi = float_key(v_hi) + 1u;
+    above = forced;
+    for (int step = 0; !exact && hi - lo > 1u; ++step) {
+      const uint32_t mid = key_between(lo, hi, step);
+      const float v = key_value(mid);
+      int c = 0;
+      for (int j = lane; j < n; j += 32) c += kr[j] >= v;
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c >= p.n_sel) {
+        lo = mid;
+        exact = c == p.n_sel;
+      } else {
+        hi = mid;
+        above = c;
+      }
     }
+    thr = key_value(lo);
   }
-  const int want = exact ? p.n_sel : p.n_sel - above;
-  int at = 0, ties = 0;
-#pragma unroll 2
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t key = j < n ? kr[j] : 0u;
-    const bool gt = j < n && (exact ? key >= low : key > low), eq = j < n && !exact && key == low;
-    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (!(bg | be)) continue;
-    const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
-    if (gt) out[g0 + min(e0, want)] = j;
-    else if (eq && e0 < want) out[g0 + e0] = j;
-    at += __popc(bg);
-    ties += __popc(be);
+  // ---- ordered output: lane i holds the bits of the taken pages 32 i .. of a
+  // run of 1,024; equal scores are taken from the lowest page on
+  int want = exact ? n : p.n_sel - above, at = 0;
+  for (int base = 0; base < n; base += 1024) {
+    unsigned gt = 0, eq = 0;
+    const int words = min(32, (n - base + 31) / 32);
+#pragma unroll 4
+    for (int w = 0; w < words; ++w) {
+      const int j = base + w * 32 + lane;
+      const float x = j < n ? kr[j] : -INFINITY;
+      const unsigned bg = __ballot_sync(0xffffffffu, j < n && x > thr), be = __ballot_sync(0xffffffffu, j < n && x == thr);
+      if (lane == w) { gt = bg; eq = be; }
+    }
+    int ties = __popc(eq), tsum = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, tsum, o);
+      if (lane >= o) tsum += y;
+    }
+    for (int drop = min(ties, max(0, tsum - want)); drop > 0; --drop) eq &= ~(0x80000000u >> __clz(eq));
+    want -= __shfl_sync(0xffffffffu, tsum, 31);
+    want = max(want, 0);
+    unsigned bits = gt | eq;
+    int cnt = __popc(bits), csum = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, csum, o);
+      if (lane >= o) csum += y;
+    }
+    int to = at + csum - cnt;
+    while (bits) {
+      out[to++] = base + lane * 32 + __ffs(bits) - 1;
+      bits &= bits - 1;
+    }
+    at += __shfl_sync(0xffffffffu, csum, 31);
   }
 }
 
@@ -886,7 +927,7 @@ dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, con
   const bool d64 = kv->D == 64;
   // Eight rows share a block when sequences have that many rows and the keys
   // of eight rows fit in shared memory; otherwise each row has a cluster.
-  p.key_stride = (max_n + 3) / 4 * 4;
+  p.key_stride = (max_n + 31) / 32 * 32 + 4;  // (a lane's rows start in different banks)
   cudaError_t e;
   if (batch->max_Lq >= 4 && kSelRows * p.key_stride * 4 <= 200 * 1024) {
     p.row_blocks = (batch->max_Lq + kSelRows - 1) / kSelRows;
