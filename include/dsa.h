@@ -266,7 +266,7 @@ dsa_status dsa_mx_quantize(const dsa_bf16 *x, int64_t rows, int cols, int fmt,
  *   DSA_KV_BF16: bf16 values; k_scale and v_scale are NULL.
  *   DSA_KV_E4M3: 8-bit E4M3 codes with one f32 scale for each page and head,
  *     k_scale and v_scale [n_pages, n_kv]; value = code * scale.  Attention
- *     takes any positive finite scales; dsa_paged_append writes powers of two.
+ *     takes scales from 2^-100 to 2^120; dsa_paged_append writes powers of two.
  *   sum [n_pages, n_kv, D] int8 and sum_scale [n_pages, n_kv] f32 hold one
  *     summary for each COMPLETE page: sum * sum_scale is the mean of the
  *     page's cached keys rounded to whole steps of amax / 127.  Both NULL when
@@ -372,8 +372,9 @@ dsa_status dsa_page_topk(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
  * outside the row's visible pages are skipped, as -1 is).  A row that sees
  * nothing gets out = 0 and lse = -inf.
  * Numerics: scores are f32 sums of exact products; the softmax runs in f32;
- * the weights enter the P.V product with 8 significant bits (bf16, or two
- * E4M3 terms for an 8-bit cache), accumulated in f32; out is rounded once.
+ * the weights enter the P.V product with at least 8 significant bits (bf16,
+ * f16, or two terms of a narrower type), accumulated in f32; out is rounded
+ * once.
  *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written); lse
  *   [total_q, n_h] f32 (written; may be NULL).
  * Supported: n_h a multiple of n_kv, n_h <= 128; n_sel <= 1024.

@@ -190,6 +190,9 @@ struct Cfg {
   static constexpr int kCtasPerSm = SPARSE && NH == 8 && F8 ? 3 : NH <= 16 ? 2 : 1;
   static constexpr int kElem = F8 ? 1 : 2;
   static constexpr int kN = F8 ? 2 * NH : (NH < 16 ? 16 : NH);  // MMA columns
+  // Weights as two terms: always for an 8-bit cache; for a bf16 cache where
+  // the second fits in columns that the tile has anyway (N >= 16).
+  static constexpr bool kTwo = F8 || NH < 16;
   static constexpr int kRow = D * kElem;                        // bytes of a cached row
   static constexpr int kRowB = kRow < 128 ? kRow : 128;         // bytes of a row in a tile slab
   static constexpr int kSlabs = kRow / kRowB;
@@ -256,8 +259,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  if constexpr (C::kN > NH && !F8)  // the padding rows of Q and P stay zero
-    for (int i = threadIdx.x; i < (C::kQBytes + 2 * C::kPBytes) / 16; i += C::kThreads)
+  if constexpr (C::kN > NH && !F8)  // the padding rows of Q stay zero
+    for (int i = threadIdx.x; i < C::kQBytes / 16; i += C::kThreads)
       reinterpret_cast<uint4*>(q_smem)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -593,10 +596,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
               w[e] = ex2_approx(x[h + e] - bc[h + e]);
               l[h + e] += w[e];
             }
-            const uint32_t two = pack_bf16(w[0], w[1]);
+            const uint32_t hi = pack_bf16(w[0], w[1]);
             uint8_t* dst = pb + (key >> 6) * (C::kN * 128);
-            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h, (key & 63) * 2)) = static_cast<uint16_t>(two);
-            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(two >> 16);
+            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h, (key & 63) * 2)) = static_cast<uint16_t>(hi);
+            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(hi >> 16);
+            if constexpr (C::kTwo) {
+              const uint32_t lo = pack_bf16(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xffff0000u));
+              *reinterpret_cast<uint16_t*>(dst + op_off<128>(NH + gh + h, (key & 63) * 2)) = static_cast<uint16_t>(lo);
+              *reinterpret_cast<uint16_t*>(dst + op_off<128>(NH + gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(lo >> 16);
+            }
           }
         }
         // ---- O follows a new reference exponent
@@ -675,13 +683,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
       tc_fence_after();
       float o[HG];
-      if constexpr (F8) {
+      if constexpr (C::kTwo) {
         uint32_t a[HG], b[HG];
         tmem_ld32<HG>(tmem_o + lanes + gh, a);
         tmem_ld32<HG>(tmem_o + lanes + NH + gh, b);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < HG; ++h) o[h] = any ? fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) : 0.f;
+        for (int h = 0; h < HG; ++h) o[h] = any ? fmaf(__uint_as_float(b[h]), F8 ? 1.f / 32 : 1.f, __uint_as_float(a[h])) : 0.f;
       } else {
         uint32_t a[HG];
         tmem_ld32<HG>(tmem_o + lanes + gh, a);
