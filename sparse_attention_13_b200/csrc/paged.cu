@@ -66,6 +66,7 @@ struct AppendParams {
   const float *cos, *sin;
   int n_h, half, interleaved, n_pos;
   int touched;     // pages a sequence can touch
+  int packed;      // ragged: blocks count the pages in all instead
   int64_t units;   // blocks of cache pages: every period-th; the others rotate q
   int period;
   int q_runs, q_heads;  // runs of heads a row is cut into, heads of a run
@@ -212,7 +213,16 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged
   u >>= 1;
   const int head = u % p.a.n_kv;
   u /= p.a.n_kv;
-  const int tp = u % p.touched, b = u / p.touched;
+  int tp = u % p.touched, b = u / p.touched;
+  if (p.packed) {  // u counts the pages that the sequences really touch
+    const bool some = paged_block(p.a, u, [&](int s) {
+      int r, rows;
+      paged_rows(p.a, s, r, rows);
+      const int at = max(__ldg(p.a.sp + s), 0) % PAGE;
+      return rows ? (at + rows - 1) / PAGE + 1 : 0;
+    }, b, tp);
+    if (!some) return;
+  }
   int r0, n;
   paged_rows(p.a, b, r0, n);
   const int sp = __ldg(p.a.sp + b);
@@ -373,7 +383,7 @@ struct SelParams {
   const dsa_bf16* q;
   int n_h, page, shift, inclusive, n_sel, n_first, n_last;
   int ranks;                   // blocks of a decode row's cluster
-  int row_blocks, key_stride;  // many rows: blocks of a sequence, keys of a row
+  int key_stride;              // keys of a row in shared memory
   int32_t* sel;
 };
 
@@ -663,11 +673,14 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
   pdl_trigger();
   pdl_wait();
   const int head = blockIdx.x % p.a.n_kv;
-  const int rest = blockIdx.x / p.a.n_kv;
-  const int b = rest / p.row_blocks;
-  int r0, rows;
+  int b, blk, r0, rows;
+  const bool some = paged_block(p.a, blockIdx.x / p.a.n_kv, [&](int s) {
+    paged_rows(p.a, s, r0, rows);
+    return (rows + kSelRows - 1) / kSelRows;
+  }, b, blk);
+  if (!some) return;
   paged_rows(p.a, b, r0, rows);
-  const int first = rest % p.row_blocks * kSelRows;
+  const int first = blk * kSelRows;
   const int nr = min(kSelRows, rows - first);
   if (nr <= 0) return;
   const auto pages_of = [&](int r) { return (paged_visible(p.a, b, first + r, p.inclusive) + p.page - 1) >> p.shift; };
@@ -887,7 +900,12 @@ dsa_status dsa_paged_append(const dsa_paged_kv* kv, const dsa_paged_batch* batch
   p.k_stride = k_row_stride; p.v_stride = v_row_stride; p.q_stride = q_row_stride;
   p.cos = cos; p.sin = sin; p.n_h = n_h; p.half = rot / 2; p.interleaved = interleaved; p.n_pos = n_pos;
   p.touched = (batch->max_Lq + kv->page - 2) / kv->page + 1;
-  p.units = 2ll * batch->B * p.touched * kv->n_kv;
+  // A sequence of n rows touches at most n / page + 2 pages: in all no more
+  // than this, however long the longest sequence is.
+  const int64_t most = batch->total_q / kv->page + 2ll * std::min(batch->B, batch->total_q);
+  p.packed = static_cast<int64_t>(batch->B) * p.touched > most;
+  p.units = 2ll * kv->n_kv * (p.packed ? most : static_cast<int64_t>(batch->B) * p.touched);
+  if (p.units > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_paged_append: batch too large");
   // queries: long runs of heads reuse a row's angles; few rows are cut into
   // short runs so that some 2,000 warps share the work
   const int step = 512 / kv->D;  // heads of a warp's step
@@ -930,8 +948,7 @@ dsa_status dsa_page_topk(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, con
   p.key_stride = (max_n + 31) / 32 * 32 + 4;  // (a lane's rows start in different banks)
   cudaError_t e;
   if (batch->max_Lq >= 4 && kSelRows * p.key_stride * 4 <= 200 * 1024) {
-    p.row_blocks = (batch->max_Lq + kSelRows - 1) / kSelRows;
-    const int64_t grid = static_cast<int64_t>(batch->B) * p.row_blocks * kv->n_kv;
+    const int64_t grid = (static_cast<int64_t>(batch->total_q) / kSelRows + std::min(batch->B, batch->total_q)) * kv->n_kv;
     if (grid > 2147483647ll) return set_error(DSA_ERR_UNSUPPORTED, "dsa_page_topk: too many rows");
     auto fn = d64 ? page_topk_rows_kernel<64> : page_topk_rows_kernel<128>;
     const int smem = kSelRows * p.key_stride * 4;

@@ -56,6 +56,34 @@ __device__ __forceinline__ int paged_page(const PagedArgs& a, int b, int j) {
   return p >= 0 && p < a.n_pages ? p : -1;
 }
 
+// Blocks of work of a ragged batch in a row: block idx of the concatenation of
+// count(b) blocks per sequence is block blk of sequence b.  The grid is then
+// as large as the rows are in all, not as the longest sequence times the batch.
+// All lanes of a warp call together; false beyond the last block.
+template <typename Count>
+__device__ __forceinline__ bool paged_block(const PagedArgs& a, int64_t idx, Count count, int& b, int& blk) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  for (int s0 = 0; s0 < a.B; s0 += 32) {
+    const int own = s0 + lane < a.B ? count(s0 + lane) : 0;
+    int64_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, base + incl > idx);
+    if (over) {
+      const int f = __ffs(over) - 1;
+      b = s0 + f;
+      blk = static_cast<int>(idx - base - __shfl_sync(0xffffffffu, incl - own, f));
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll

@@ -11,7 +11,8 @@ struct PrefillParams {
   PagedArgs a;
   const dsa_bf16* q;
   int n_h, G, page, shift, ppt, inclusive;  // shift: log2 page; ppt: pages per tile
-  int tok, blocks, splits;                  // tokens of a Q tile, blocks of two tiles, parts of the keys
+  int tok, splits;                          // tokens of a Q tile, parts of the keys
+  long long blocks;                         // blocks of two Q tiles of the batch, at most
   float scale_log2;
   dsa_bf16* out;
   float* lse;
@@ -20,8 +21,8 @@ struct PrefillParams {
 };
 
 struct PrefillPlan {
-  int tok, blocks, splits;
-  long long units;
+  int tok, splits;
+  long long blocks, units;
   size_t o_bytes, l_bytes;
   size_t total() const { return o_bytes + l_bytes; }
 };

@@ -136,6 +136,17 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
   return h;
 }
+// Block id / n_kv of the batch: its sequence and number there; returns the
+// sequence's last block, or -1 beyond the batch.
+__device__ __forceinline__ int prefill_block(const PrefillParams& p, int64_t id, int& b, int& blk) {
+  int r0, n;
+  const auto blocks = [&](int s) {
+    paged_rows(p.a, s, r0, n);
+    return (n + 2 * p.tok - 1) / (2 * p.tok);
+  };
+  return paged_block(p.a, id / p.a.n_kv, blocks, b, blk) ? blocks(b) - 1 : -1;
+}
+
 // Adds the values of positions [s0, s1) that are not finite to a row's output
 // (the tiles held zeros in their place, because other rows do not see them).
 template <int D, bool F8>
@@ -200,20 +211,19 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   pdl_trigger();
   pdl_wait();
 
-  // the unit of this CTA: late blocks first (they see the most keys)
+  // the unit of this CTA
   Unit u;
   const int split = blockIdx.x % p.splits;
-  int64_t id = blockIdx.x / p.splits;
+  const int64_t id = blockIdx.x / p.splits;
   {
-    const int per = p.a.B * p.a.n_kv;
-    const int blk = p.blocks - 1 - static_cast<int>(id / per);
+    int r0 = 0, n = 0, blk = 0;
     u.kvh = static_cast<int>(id % p.a.n_kv);
-    u.b = static_cast<int>(id % per) / p.a.n_kv;
-    int r0, n;
-    paged_rows(p.a, u.b, r0, n);
-    const int first = blk * 2 * p.tok;
+    u.b = 0;
+    const int last = prefill_block(p, id, u.b, blk);
+    if (last >= 0) paged_rows(p.a, u.b, r0, n);
+    const int first = (last - blk) * 2 * p.tok;  // late blocks first (they see the most keys)
     u.row0 = r0 + first;
-    u.rows = max(0, min(2 * p.tok, n - first));
+    u.rows = last < 0 ? 0 : max(0, min(2 * p.tok, n - first));
     u.nq = u.rows > p.tok ? 2 : (u.rows > 0 ? 1 : 0);
     u.t0 = u.t1 = 0;
     u.lo = u.hi[0] = u.hi[1] = 0;
@@ -626,14 +636,14 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
   constexpr int kVecs = D / 4, kRows = 128 / kVecs;
   pdl_trigger();
   pdl_wait();
-  const int per = p.a.B * p.a.n_kv;
   const int64_t tile = blockIdx.x / (128 / kRows), id = tile / 2;
   const int q = static_cast<int>(tile & 1), m = blockIdx.x % (128 / kRows) * kRows + threadIdx.x / kVecs, v = threadIdx.x % kVecs;
-  const int blk = p.blocks - 1 - static_cast<int>(id / per), kvh = static_cast<int>(id % p.a.n_kv);
-  const int b = static_cast<int>(id % per) / p.a.n_kv;
-  int r0, n;
+  const int kvh = static_cast<int>(id % p.a.n_kv);
+  int b, blk, r0, n;
+  const int last = prefill_block(p, id, b, blk);
+  if (last < 0) return;
   paged_rows(p.a, b, r0, n);
-  const int tok = m / p.G, row = blk * 2 * p.tok + q * p.tok + tok;
+  const int tok = m / p.G, row = (last - blk) * 2 * p.tok + q * p.tok + tok;
   if (tok >= p.tok || row >= n) return;
   const auto at = [&](int s) { return ((id * p.splits + s) * 2 + q) * 128 + m; };
   float top = -INFINITY;
@@ -657,7 +667,7 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
 template <int D, bool F8>
 cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PrefillParams& p, cudaStream_t s) {
   using C = PreCfg<D, F8>;
-  const int64_t units = static_cast<int64_t>(p.blocks) * p.a.B * p.a.n_kv;
+  const int64_t units = p.blocks * p.a.n_kv;
   auto fn = paged_prefill_kernel<D, F8>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), C::kSmem);
   if (e == cudaSuccess) e = launch_pdl(fn, dim3(static_cast<unsigned>(units * p.splits)), dim3(kThreads), C::kSmem, s, k, v, p);
@@ -672,8 +682,9 @@ PrefillPlan paged_prefill_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb
   PrefillPlan pl{};
   const int G = n_h / kv->n_kv;
   pl.tok = 128 / G;
-  pl.blocks = (pb->max_Lq + 2 * pl.tok - 1) / (2 * pl.tok);
-  const int64_t units = static_cast<int64_t>(pl.blocks) * pb->B * kv->n_kv;
+  // a sequence of n rows has at most n / (2 tok) + 1 blocks
+  pl.blocks = pb->total_q / (2 * pl.tok) + std::min(pb->B, pb->total_q);
+  const int64_t units = pl.blocks * kv->n_kv;
   pl.units = units;
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;

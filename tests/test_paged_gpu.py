@@ -544,3 +544,42 @@ def test_serving_loop(dsa, fmt):
         _check_attn(dsa, kv, seen, batch, table, lens, starts, qr.cpu(), 1 / 8, True, sel=sel.cpu(), rows=rows)
         _check_attn(dsa, kv, seen, batch, table, lens, starts, qr.cpu(), 1 / 8, True, rows=rows)
         starts, lens = [s + n for s, n in zip(starts, lens)], [1, 1, 1]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_one_long_chunk_among_many_short_sequences(dsa, fmt):
+    # 70 sequences (more than a warp looks at in one go), most with one row or
+    # none, one with 300: every operator finds its rows
+    g = _gen(21)
+    q_lens = [1] * 70
+    q_lens[41], q_lens[3], q_lens[69], q_lens[33] = 300, 0, 0, 17
+    starts = [int(x) for x in torch.randint(0, 200, (70,), generator=g)]
+    starts[0], starts[41] = 0, 90
+    page, n_kv, n_h, D = 16, 2, 8, 64
+    ends = [s + n for s, n in zip(starts, q_lens)]
+    table, t, n_pages = _table(ends, [0] * 70, page, g)
+    kv = _pool(dsa, n_pages, page, n_kv, D, fmt)
+    mirror = ref.Cache(kv)
+    for lens, begin in ((starts, [0] * 70), (q_lens, starts)):
+        batch = dsa.PagedBatch.from_lens(lens, begin, t)
+        k, v = _bf16(g, sum(lens), n_kv, D), _bf16(g, sum(lens), n_kv, D)
+        before = {n: getattr(kv, n).cpu().clone() for n in ("k", "v")}
+        dsa.paged_append(kv, batch, k.cuda(), v.cuda())
+        touched = set()
+        mirror.append(lens, begin, table, k, v, None, None, False, touched)
+        _check_cache(kv, mirror, touched, before)
+    assert dsa.check_paged(kv, batch) == 0
+    seen = ref.Cache(kv)
+    q = _bf16(g, sum(q_lens), n_h, D)
+    sel = dsa.page_topk(q.cuda(), kv, batch, 4, inclusive=True).cpu()
+    r = 0
+    for b, n in enumerate(q_lens):
+        for i in range(n):
+            vis = -(-(starts[b] + i + 1) // page)
+            for h in range(n_kv):
+                pages = table[b][:vis]
+                assert sel[r, h].tolist() == ref.select_row(q[r, 4 * h:4 * h + 4].double(), seen.sum[pages, h], seen.sum_scale[pages, h], vis, 4, 1, 1)
+            r += 1
+    rows = set(torch.randperm(sum(q_lens), generator=g)[:60].tolist()) | {0, sum(q_lens) - 1}
+    _check_attn(dsa, kv, seen, batch, table, q_lens, starts, q, 0.125, True, rows=rows)
+    _check_attn(dsa, kv, seen, batch, table, q_lens, starts, q, 0.125, True, sel=sel, rows=rows)
