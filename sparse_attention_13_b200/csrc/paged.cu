@@ -136,7 +136,7 @@ __device__ __forceinline__ float block_max(float x, float* red) {
 // 8 columns of every (256 / (D/8))-th slot, in registers from the load to the
 // store.  Bound by memory: new rows in, cache rows out, each once.
 template <int D, int PAGE, bool F8>
-__global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;                    // threads per slot
   constexpr int kRows = kAppendThreads / kVecs;   // slots per step
   constexpr int kSteps = PAGE > kRows ? PAGE / kRows : 1;
@@ -176,34 +176,46 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged
       }
     }
     const int h_end = min(p.n_h, static_cast<int>(w % p.q_runs + 1) * p.q_heads);
-#pragma unroll 4
-    for (int h = static_cast<int>(w % p.q_runs) * p.q_heads + lane / kLanes; h < h_end; h += kHeads) {
-      const dsa_bf16* x = p.q + row * p.q_stride + h * D;
-      uint4 u0 = *reinterpret_cast<const uint4*>(x + c0), u1 = *reinterpret_cast<const uint4*>(x + c1);
-      if (turn) {
-        float f[16];
-        bf16x8_to_f32(u0, *reinterpret_cast<float(*)[8]>(f));
-        bf16x8_to_f32(u1, *reinterpret_cast<float(*)[8]>(f + 8));
-        float g[16];
+    // (the loads of a batch of heads come first: stores to q_out, which may be
+    // q, would hold back the loads behind them)
+    constexpr int kBatch = 4;
+    for (int h0 = static_cast<int>(w % p.q_runs) * p.q_heads + lane / kLanes; h0 < h_end; h0 += kBatch * kHeads) {
+      uint4 u0[kBatch], u1[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float ua = p.interleaved ? f[2 * e] : f[e], ub = p.interleaved ? f[2 * e + 1] : f[e + 8];
-          const float ra = __fsub_rn(__fmul_rn(ua, cc[e]), __fmul_rn(ub, ss[e]));
-          const float rb = __fadd_rn(__fmul_rn(ub, cc[e]), __fmul_rn(ua, ss[e]));
-          g[e] = ra;
-          g[e + 8] = rb;
-        }
-        if (p.interleaved) {
-          u0 = make_uint4(pack_bf16(g[0], g[8]), pack_bf16(g[1], g[9]), pack_bf16(g[2], g[10]), pack_bf16(g[3], g[11]));
-          u1 = make_uint4(pack_bf16(g[4], g[12]), pack_bf16(g[5], g[13]), pack_bf16(g[6], g[14]), pack_bf16(g[7], g[15]));
-        } else {
-          u0 = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
-          u1 = make_uint4(pack_bf16(g[8], g[9]), pack_bf16(g[10], g[11]), pack_bf16(g[12], g[13]), pack_bf16(g[14], g[15]));
+      for (int k = 0; k < kBatch; ++k) {
+        const int h = h0 + k * kHeads;
+        if (h < h_end) {
+          const dsa_bf16* x = p.q + row * p.q_stride + h * D;
+          u0[k] = *reinterpret_cast<const uint4*>(x + c0);
+          u1[k] = *reinterpret_cast<const uint4*>(x + c1);
         }
       }
-      dsa_bf16* y = p.q_out + (row * p.n_h + h) * D;
-      *reinterpret_cast<uint4*>(y + c0) = u0;
-      *reinterpret_cast<uint4*>(y + c1) = u1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int h = h0 + k * kHeads;
+        if (h >= h_end) break;
+        if (turn) {
+          uint32_t* w0 = &u0[k].x;
+          uint32_t* w1 = &u1[k].x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // halves: word e of both vectors, (x[2e], x[2e+1]) and their
+            // partners; interleaved: the pairs in word e of each vector
+            const float a0 = __uint_as_float(w0[e] << 16), a1 = __uint_as_float(w0[e] & 0xffff0000u);
+            const float b0 = __uint_as_float(w1[e] << 16), b1 = __uint_as_float(w1[e] & 0xffff0000u);
+            if (p.interleaved) {
+              w0[e] = pack_bf16(__fsub_rn(__fmul_rn(a0, cc[e]), __fmul_rn(a1, ss[e])), __fadd_rn(__fmul_rn(a1, cc[e]), __fmul_rn(a0, ss[e])));
+              w1[e] = pack_bf16(__fsub_rn(__fmul_rn(b0, cc[e + 4]), __fmul_rn(b1, ss[e + 4])), __fadd_rn(__fmul_rn(b1, cc[e + 4]), __fmul_rn(b0, ss[e + 4])));
+            } else {
+              w0[e] = pack_bf16(__fsub_rn(__fmul_rn(a0, cc[2 * e]), __fmul_rn(b0, ss[2 * e])), __fsub_rn(__fmul_rn(a1, cc[2 * e + 1]), __fmul_rn(b1, ss[2 * e + 1])));
+              w1[e] = pack_bf16(__fadd_rn(__fmul_rn(b0, cc[2 * e]), __fmul_rn(a0, ss[2 * e])), __fadd_rn(__fmul_rn(b1, cc[2 * e + 1]), __fmul_rn(a1, ss[2 * e + 1])));
+            }
+          }
+        }
+        dsa_bf16* y = p.q_out + (row * p.n_h + h) * D;
+        *reinterpret_cast<uint4*>(y + c0) = u0[k];
+        *reinterpret_cast<uint4*>(y + c1) = u1[k];
+      }
     }
     return;
   }
@@ -230,12 +242,9 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged
   const int j = sp / PAGE + tp;              // page of the sequence
   const int first = max(sp, j * PAGE), end = min(sp + n, (j + 1) * PAGE);
   if (first >= end) return;
-  const int pg = paged_page(p.a, b, j);
-  if (pg < 0) return;
+  const int pg = paged_page(p.a, b, j);  // (used after the rows, whose loads need not wait for it)
   const int a0 = first - j * PAGE, a1 = end - j * PAGE;  // new slots of the page
   const bool whole = !is_v && a1 == PAGE && p.a.sum;
-  const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
-  const int64_t base = unit * PAGE * D;
 
   float f[kSteps][8];
   float amax = 0.f;
@@ -256,6 +265,9 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged
     }
   }
 
+  if (pg < 0) return;
+  const int64_t unit = static_cast<int64_t>(pg) * p.a.n_kv + head;
+  const int64_t base = unit * PAGE * D;
   float scale = 1.f, ratio = 1.f;
   if constexpr (F8) {
     float* sc = (is_v ? p.a.v_scale : p.a.k_scale) + unit;
@@ -328,34 +340,25 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 4) paged
   for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = f[0][i];
   __syncthreads();
   constexpr int kGroups = PAGE < kRows ? PAGE : kRows;
-  for (int h = kGroups / 2; h; h >>= 1) {
-    if (g < h)
+  const int col = threadIdx.x;  // a thread per column from here on
+  float x = 0.f;
+  if (col < D) {
+    float v[kGroups];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = __fadd_rn(part[threadIdx.x][i], part[threadIdx.x + h * kVecs][i]);
-    __syncthreads();
-  }
-  float top = 0.f;
-  bool fine = true;
+    for (int i = 0; i < kGroups; ++i) v[i] = part[i * kVecs + col / 8][col % 8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = __fmul_rn(part[vec][i], scale);
-    f[0][i] = x;
-    fine = fine && fabsf(x) <= kMaxF32;
-    top = fmaxf(top, fabsf(x));
+    for (int h = kGroups / 2; h; h >>= 1)
+#pragma unroll
+      for (int i = 0; i < kGroups / 2; ++i)
+        if (i < h) v[i] = __fadd_rn(v[i], v[i + h]);
+    x = __fmul_rn(v[0], scale);
   }
-  fine = __syncthreads_and(fine);
-  top = block_max(top, red);
+  bool fine = __syncthreads_and(fabsf(x) <= kMaxF32);
+  const float top = block_max(fabsf(x), red);
   fine = fine && top >= kMinTop;
-  if (g == 0) {
-    const float inv = __fmul_rn(127.f, __frcp_rn(top));
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int code = fine ? __float2int_rn(__fmul_rn(f[0][i], inv)) : 0;
-      w[i >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (i & 3));
-    }
-    *reinterpret_cast<uint2*>(p.a.sum + unit * D + c) = make_uint2(w[0], w[1]);
-    if (vec == 0) p.a.sum_scale[unit] = fine ? __fmul_rn(__fmul_rn(top, 1.f / 127.f), 1.f / PAGE) : 0.f;
+  if (col < D) {
+    p.a.sum[unit * D + col] = fine ? static_cast<int8_t>(__float2int_rn(__fmul_rn(x, __fmul_rn(127.f, __frcp_rn(top))))) : 0;
+    if (col == 0) p.a.sum_scale[unit] = fine ? __fmul_rn(__fmul_rn(top, 1.f / 127.f), 1.f / PAGE) : 0.f;
   }
 }
 
