@@ -76,14 +76,16 @@ constexpr int kAppendThreads = 256;
 constexpr float kMaxF32 = 3.402823466e38f;
 constexpr float kMinTop = 3.8e-37f;  // 127 * (1 / amax) stays finite above it
 
-// Eight consecutive columns (from column c) of a head's row x, rotated by the
-// angles of position pos.  Products and sums are rounded one by one (no fused
-// multiply-add), so that the result does not depend on the compiler.
-__device__ __forceinline__ void rotated8(const dsa_bf16* x, int c, int pos, const AppendParams& p, float (&f)[8]) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(x + c), f);
-  if (c >= 2 * p.half) return;
+// Rotates the eight columns of vector `vec` of a head's row (raw: the bf16
+// columns, f: the same in f32) by the angles of position pos.  A pair's other
+// half is in another lane of the row.  Products and sums are rounded one by one
+// (no fused multiply-add), so that the result does not depend on the compiler.
+__device__ __forceinline__ void rotate8(const uint4& raw, int vec, int pos, const AppendParams& p, float (&f)[8]) {
   const int64_t at = static_cast<int64_t>(pos) * p.half;
+  const int c = 8 * vec;
+  const bool turn = c < 2 * p.half;
   if (p.interleaved) {
+    if (!turn) return;
     const float4 cs = __ldg(reinterpret_cast<const float4*>(p.cos + at + c / 2));
     const float4 sn = __ldg(reinterpret_cast<const float4*>(p.sin + at + c / 2));
     const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
@@ -96,9 +98,16 @@ __device__ __forceinline__ void rotated8(const dsa_bf16* x, int c, int pos, cons
     return;
   }
   const bool low = c < p.half;
-  const int pair = low ? c : c - p.half;
+  const int lane = threadIdx.x & 31, src = !turn ? lane : lane + (low ? p.half / 8 : -p.half / 8);
+  uint4 other;
+  other.x = __shfl_sync(0xffffffffu, raw.x, src);
+  other.y = __shfl_sync(0xffffffffu, raw.y, src);
+  other.z = __shfl_sync(0xffffffffu, raw.z, src);
+  other.w = __shfl_sync(0xffffffffu, raw.w, src);
+  if (!turn) return;
   float o[8];
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(x + (low ? c + p.half : pair)), o);
+  bf16x8_to_f32(other, o);
+  const int pair = low ? c : c - p.half;
   const float4* cs4 = reinterpret_cast<const float4*>(p.cos + at + pair);
   const float4* sn4 = reinterpret_cast<const float4*>(p.sin + at + pair);
   const float4 c0 = __ldg(cs4), c1 = __ldg(cs4 + 1), s0 = __ldg(sn4), s1 = __ldg(sn4 + 1);
@@ -246,22 +255,27 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged
   const int a0 = first - j * PAGE, a1 = end - j * PAGE;  // new slots of the page
   const bool whole = !is_v && a1 == PAGE && p.a.sum;
 
+  // all rows of the thread are in flight before the first is used
+  uint4 raw[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int slot = s * kRows + g;
+    raw[s] = make_uint4(0, 0, 0, 0);
+    if (slot >= a0 && slot < a1) {
+      const int64_t row = r0 + (j * PAGE + slot - sp);
+      raw[s] = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) + head * D + c));
+    }
+  }
   float f[kSteps][8];
   float amax = 0.f;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
     const int slot = s * kRows + g;
+    bf16x8_to_f32(raw[s], f[s]);
+    if (!is_v && p.half) rotate8(raw[s], vec, j * PAGE + min(max(slot, a0), a1 - 1), p, f[s]);
+    if constexpr (F8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[s][i] = 0.f;
-    if (slot >= a0 && slot < a1) {
-      const int pos = j * PAGE + slot;
-      const int64_t row = r0 + (pos - sp);
-      if (is_v) bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + head * D + c)), f[s]);
-      else rotated8(p.k + row * p.k_stride + head * D, c, pos, p, f[s]);
-      if constexpr (F8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[s][i]) <= kMaxF32 ? fabsf(f[s][i]) : 0.f);
-      }
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[s][i]) <= kMaxF32 ? fabsf(f[s][i]) : 0.f);
     }
   }
 
