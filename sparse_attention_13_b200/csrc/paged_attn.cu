@@ -31,7 +31,7 @@ struct PattnParams {
   const int32_t* sel;
   int n_h, G, page, shift, ppt, inclusive, n_sel;  // shift: log2 page; ppt: pages per tile
   int Gx, R, hbs, max_rb;  // heads and rows of a unit, head blocks, row blocks
-  int tpu, aligned;        // sparse: tiles per unit; whole units per CTA
+  int tpu, aligned;        // sparse: tiles per unit; CTAs take whole units
   float scale_log2;
   dsa_bf16* out;
   float* lse;
@@ -67,7 +67,8 @@ struct Walker {
   __device__ __forceinline__ long long seq(int s, int& r, int& rows, int& blocks, int& t) const {
     paged_rows(p.a, s, r, rows);
     blocks = (rows + p.R - 1) / p.R;
-    t = rows ? max(1, (paged_visible(p.a, s, rows - 1, p.inclusive) + kTile - 1) / kTile) : 1;
+    // (where CTAs take whole units, a unit counts as one)
+    t = rows && !p.aligned ? max(1, (paged_visible(p.a, s, rows - 1, p.inclusive) + kTile - 1) / kTile) : 1;
     return static_cast<long long>(blocks) * p.a.n_kv * p.hbs * t;
   }
 
@@ -174,7 +175,7 @@ struct Walker {
     if constexpr (!SPARSE) {  // earlier rows end earlier than the sequence
       const int own = max(1, (s.t1 + kTile - 1) / kTile);
       s.lo = min(s.lo, own);
-      s.hi = min(s.hi, own);
+      s.hi = p.aligned ? own : min(s.hi, own);
     }
     return true;
   }
@@ -835,7 +836,11 @@ Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n
   // many units of selected 8-bit pages run three CTAs to an SM (latency-bound:
   // 1359 -> 1157 us for 16,384 units of 16 tiles)
   const int ctas = n_sel && pl.NH == 8 && kv->fmt == DSA_KV_E4M3 && pl.units >= 8ll * two ? std::min(kMaxCtas, sms * 3) : two;
-  pl.aligned = n_sel && pl.units >= 8ll * ctas;
+  // Whole units per CTA and no merge: for units of a few tiles (1 x 8 heads x 500
+  // tokens: 9.8 us whole, 10.4 us cut; 1,000 tokens 14.3 and 10.8), a few more
+  // where the units occupy a third of the GPU (16 x 8 heads x 1,000 tokens: 15.5
+  // and 17.6), and for many equal units of selected pages.
+  pl.aligned = pl.tpu <= 4 || (pl.tpu <= 8 && pl.units * 3 >= ctas) || (n_sel && pl.units >= 8ll * ctas);
   pl.grid = static_cast<int>(std::min<long long>(ctas, pl.aligned ? pl.units : std::max(1ll, pl.units * pl.tpu / 2)));
   pl.merge = !pl.aligned && pl.grid > 1;
   if (pl.merge) {
