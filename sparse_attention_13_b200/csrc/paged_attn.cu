@@ -172,11 +172,29 @@ struct Walker {
         }
       }
     }
-    if constexpr (!SPARSE) {  // earlier rows end earlier than the sequence
-      const int own = max(1, (s.t1 + kTile - 1) / kTile);
-      s.lo = min(s.lo, own);
+    // the unit's own tiles: earlier rows end earlier than the sequence, and a
+    // list that is longer than the row's pages ends with its last valid entry
+    int own;
+    if constexpr (SPARSE) {
+      own = nominal;
+      const int n_vis = (s.t1 + p.page - 1) >> p.shift;
+      if (n_vis < p.n_sel) {
+        const int32_t* list = p.sel + (static_cast<int64_t>(s.row0) * p.a.n_kv + s.kvh) * p.n_sel;
+        int l0 = (p.n_sel - 1) / 32 * 32, last = -1;
+        for (; l0 >= 0 && last < 0; l0 -= 32) {
+          const int l = l0 + (static_cast<int>(threadIdx.x) & 31);
+          const int e = l < p.n_sel ? __ldg(list + l) : -1;
+          const unsigned m = __ballot_sync(0xffffffffu, e >= 0 && e < n_vis);
+          if (m) last = l0 + 31 - __clz(m);
+        }
+        own = last < 0 ? 1 : (last * p.page) / kTile + 1;
+      }
+      s.hi = min(s.hi, own);
+    } else {
+      own = max(1, (s.t1 + kTile - 1) / kTile);
       s.hi = p.aligned ? own : min(s.hi, own);
     }
+    s.lo = min(s.lo, own);
     return true;
   }
 };

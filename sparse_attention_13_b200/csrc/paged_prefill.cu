@@ -689,7 +689,7 @@ PrefillPlan paged_prefill_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
   const int tiles = (pb->max_Lk + kTile - 1) / kTile;
-  pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, tiles / 8)));
+  pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, tiles / 3)));
   if (pl.splits > 1) {
     pl.o_bytes = static_cast<size_t>(units) * pl.splits * 256 * kv->D * 4;
     pl.l_bytes = static_cast<size_t>(units) * pl.splits * 256 * 4;
