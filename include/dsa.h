@@ -286,7 +286,7 @@ dsa_status dsa_mx_quantize(const dsa_bf16 *x, int64_t rows, int cols, int fmt,
  * entries of the pages that hold positions below start_pos[b] + rows name
  * pages of the pool.  A batch that breaks it gets unspecified rows but no
  * access outside the tensors.  Several sequences may share a page that is only
- * read; a page that a call appends to belongs to one sequence.
+ * read; a page that a call appends to belongs to one sequence, once.
  *
  * Visibility: row i at t = start_pos[b] + i sees s < t as everywhere in this
  * library, or s <= t when `inclusive` is 1 (its own token, which has then been
@@ -375,8 +375,8 @@ dsa_status dsa_page_topk(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
  * the weights enter the P.V product with at least 8 significant bits (bf16,
  * f16, or two terms of a narrower type), accumulated in f32; out is rounded
  * once.
- *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written); lse
- *   [total_q, n_h] f32 (written; may be NULL).
+ *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written; not q
+ *   itself); lse [total_q, n_h] f32 (written; may be NULL); 0 < scale <= 1e30.
  * Supported: n_h a multiple of n_kv, n_h <= 128; n_sel <= 1024.
  * Workspace: dsa_paged_attn_workspace() bytes, contents undefined on entry; a
  * call in flight needs a workspace of its own. */

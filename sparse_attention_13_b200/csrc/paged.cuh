@@ -63,20 +63,34 @@ __device__ __forceinline__ int paged_page(const PagedArgs& a, int b, int j) {
 template <typename Count>
 __device__ __forceinline__ bool paged_block(const PagedArgs& a, int64_t idx, Count count, int& b, int& blk) {
   const int lane = threadIdx.x & 31;
+  const int per = a.B <= 32 ? 1 : 4;  // sequences per lane (independent loads)
   int64_t base = 0;
-  for (int s0 = 0; s0 < a.B; s0 += 32) {
-    const int own = s0 + lane < a.B ? count(s0 + lane) : 0;
-    int64_t incl = own;
+  for (int s0 = 0; s0 < a.B; s0 += 32 * per) {
+    int w[4] = {0, 0, 0, 0};
+    int own = 0;  // (all counts together are below 2^31: the rows are)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int s = s0 + per * lane + e;
+      if (e < per && s < a.B) w[e] = count(s);
+      own += w[e];
+    }
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     const unsigned over = __ballot_sync(0xffffffffu, base + incl > idx);
     if (over) {
       const int f = __ffs(over) - 1;
-      b = s0 + f;
-      blk = static_cast<int>(idx - base - __shfl_sync(0xffffffffu, incl - own, f));
+      b = s0 + per * f;
+      int left = static_cast<int>(idx - base) - __shfl_sync(0xffffffffu, incl - own, f);
+#pragma unroll
+      for (int e = 0; e < 3; ++e) {
+        const int x = __shfl_sync(0xffffffffu, w[e], f);
+        if (e + 1 < per && b == s0 + per * f + e && x <= left) { left -= x; ++b; }
+      }
+      blk = left;
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

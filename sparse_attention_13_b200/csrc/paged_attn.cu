@@ -87,34 +87,53 @@ struct Walker {
       b = -1;
     } else {
       const int lane = threadIdx.x & 31;
+      // 128 sequences at a time, four per lane (independent loads)
       int r, rows, blocks, t;
-      total = 0;
-      for (int s0 = 0; s0 < p.a.B; s0 += 32) {
-        long long w = s0 + lane < p.a.B ? seq(s0 + lane, r, rows, blocks, t) : 0;
+      long long w[4];
+      const auto load = [&](int s0) {
+        long long sum = 0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-        total += w;
+        for (int e = 0; e < 4; ++e) {
+          const int s = s0 + 4 * lane + e;
+          w[e] = s < p.a.B ? seq(s, r, rows, blocks, t) : 0;
+          sum += w[e];
+        }
+        return sum;
+      };
+      total = 0;
+      long long sum = 0;
+      for (int s0 = 0; s0 < p.a.B; s0 += 128) {
+        sum = load(s0);
+        long long all = sum;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        total += all;
       }
       pos = total * c / C;
       end = total * (c + 1) / C;
       base = 0;
       b = 0;
-      for (int s0 = 0; s0 < p.a.B; s0 += 32) {  // the sequence that holds tile pos
-        long long w = s0 + lane < p.a.B ? seq(s0 + lane, r, rows, blocks, t) : 0;
-        const long long own = w;
+      for (int s0 = 0; s0 < p.a.B; s0 += 128) {  // the sequence that holds tile pos
+        if (p.a.B > 128) sum = load(s0);
+        long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, w, o);
-          if (lane >= o) w += y;
+          const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
         }
-        const unsigned over = __ballot_sync(0xffffffffu, base + w > pos);
+        const unsigned over = __ballot_sync(0xffffffffu, base + incl > pos);
         if (over) {
           const int f = __ffs(over) - 1;
-          b = s0 + f;
-          base += __shfl_sync(0xffffffffu, w - own, f);
+          b = s0 + 4 * f;
+          base += __shfl_sync(0xffffffffu, incl - sum, f);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const long long x = __shfl_sync(0xffffffffu, w[e], f);
+            if (b == s0 + 4 * f + e && base + x <= pos) { base += x; ++b; }
+          }
           break;
         }
-        base += __shfl_sync(0xffffffffu, w, 31);
+        base += __shfl_sync(0xffffffffu, incl, 31);
       }
       weight = b < p.a.B ? seq(b, r0, n, nrb, tiles) : 0;
       if (weight) {

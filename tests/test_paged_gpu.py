@@ -583,3 +583,17 @@ def test_one_long_chunk_among_many_short_sequences(dsa, fmt):
     rows = set(torch.randperm(sum(q_lens), generator=g)[:60].tolist()) | {0, sum(q_lens) - 1}
     _check_attn(dsa, kv, seen, batch, table, q_lens, starts, q, 0.125, True, rows=rows)
     _check_attn(dsa, kv, seen, batch, table, q_lens, starts, q, 0.125, True, sel=sel, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_of_many_sequences(dsa, fmt):
+    # 300 sequences with a row each, lengths from nothing to 700 tokens
+    g = _gen(22)
+    B, page, n_kv, n_h, D = 300, 32, 2, 6, 64
+    starts = [int(x) for x in torch.randint(0, 700, (B,), generator=g)]
+    starts[0] = starts[129] = starts[299] = 0
+    kv, mirror, batch, table, g = _filled(dsa, [1] * B, starts, n_kv, D, page, fmt, 23)
+    q = _bf16(g, B, n_h, D, std=1.5)
+    rows = set(torch.randperm(B, generator=g)[:60].tolist()) | {0, 1, 127, 128, 129, 298, 299}
+    for inc in (False, True):
+        _check_attn(dsa, kv, mirror, batch, table, [1] * B, starts, q, 0.125, inc, rows=rows)
