@@ -459,6 +459,13 @@ __device__ __forceinline__ void tmem_st32x16(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 
+// 32 lanes x 8 columns store.
+__device__ __forceinline__ void tmem_st32x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 32 lanes x 32 columns store (thread i writes lane base+i).
 __device__ __forceinline__ void tmem_st32x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
