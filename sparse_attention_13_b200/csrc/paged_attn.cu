@@ -615,43 +615,47 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         // ---- weights, as the MMA's B operand.  P(it - 2) has been read.
         if (it >= 2) ok = mbar_wait(&pv_done[buf], ((it - 2) >> 1) & 1, abort_flag) && ok;
         uint8_t* pb = p_smem + buf * C::kPBytes;
+        // (all computed before the first store: byte stores may alias the factors)
+        uint32_t code[HG];  // F8: a pair's hi codes, its lo codes above them; bf16: a pair's hi words, then the lo words
+#pragma unroll
+        for (int h = 0; h < HG; h += 2) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            w[e] = ex2_approx(x[h + e] - bc[h + e]);
+            l[h + e] += w[e];
+            if constexpr (F8) w[e] *= vs * bc[HG + h + e];
+          }
+          if constexpr (F8) {
+            const uint32_t hi = e4m3x2(w[0], w[1]);
+            const float2 back = e4m3x2_to_f32(hi);
+            code[h / 2] = hi | e4m3x2((w[0] - back.x) * 32.f, (w[1] - back.y) * 32.f) << 16;
+          } else {
+            const uint32_t hi = pack_bf16(w[0], w[1]);
+            code[h / 2] = hi;
+            if constexpr (C::kTwo)
+              code[HG / 2 + h / 2] = pack_bf16(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xffff0000u));
+          }
+        }
         if constexpr (F8) {
 #pragma unroll
           for (int h = 0; h < HG; h += 2) {
-            float w[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float pw = ex2_approx(x[h + e] - bc[h + e]);
-              l[h + e] += pw;
-              w[e] = pw * (vs * bc[HG + h + e]);
-            }
-            const uint32_t hi = e4m3x2(w[0], w[1]);
-            const float2 back = e4m3x2_to_f32(hi);
-            const uint32_t lo = e4m3x2((w[0] - back.x) * 32.f, (w[1] - back.y) * 32.f);
-            pb[op_off<128>(gh + h, key)] = static_cast<uint8_t>(hi);
-            pb[op_off<128>(gh + h + 1, key)] = static_cast<uint8_t>(hi >> 8);
-            pb[op_off<128>(NH + gh + h, key)] = static_cast<uint8_t>(lo);
-            pb[op_off<128>(NH + gh + h + 1, key)] = static_cast<uint8_t>(lo >> 8);
+            const uint32_t v = code[h / 2];
+            pb[op_off<128>(gh + h, key)] = static_cast<uint8_t>(v);
+            pb[op_off<128>(gh + h + 1, key)] = static_cast<uint8_t>(v >> 8);
+            pb[op_off<128>(NH + gh + h, key)] = static_cast<uint8_t>(v >> 16);
+            pb[op_off<128>(NH + gh + h + 1, key)] = static_cast<uint8_t>(v >> 24);
           }
         } else {
+          uint8_t* dst = pb + (key >> 6) * (C::kN * 128);
 #pragma unroll
-          for (int h = 0; h < HG; h += 2) {
-            float w[2];
+          for (int t = 0; t < (C::kTwo ? 2 : 1); ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              w[e] = ex2_approx(x[h + e] - bc[h + e]);
-              l[h + e] += w[e];
+            for (int h = 0; h < HG; h += 2) {
+              const uint32_t v = code[t * (HG / 2) + h / 2];
+              *reinterpret_cast<uint16_t*>(dst + op_off<128>(t * NH + gh + h, (key & 63) * 2)) = static_cast<uint16_t>(v);
+              *reinterpret_cast<uint16_t*>(dst + op_off<128>(t * NH + gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(v >> 16);
             }
-            const uint32_t hi = pack_bf16(w[0], w[1]);
-            uint8_t* dst = pb + (key >> 6) * (C::kN * 128);
-            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h, (key & 63) * 2)) = static_cast<uint16_t>(hi);
-            *reinterpret_cast<uint16_t*>(dst + op_off<128>(gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(hi >> 16);
-            if constexpr (C::kTwo) {
-              const uint32_t lo = pack_bf16(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xffff0000u));
-              *reinterpret_cast<uint16_t*>(dst + op_off<128>(NH + gh + h, (key & 63) * 2)) = static_cast<uint16_t>(lo);
-              *reinterpret_cast<uint16_t*>(dst + op_off<128>(NH + gh + h + 1, (key & 63) * 2)) = static_cast<uint16_t>(lo >> 16);
-            }
-          }
         }
         // ---- O follows a new reference exponent
         if (grew && i > cur.lo) {  // the same for the whole group
