@@ -597,3 +597,82 @@ def test_decode_of_many_sequences(dsa, fmt):
     rows = set(torch.randperm(B, generator=g)[:60].tolist()) | {0, 1, 127, 128, 129, 298, 299}
     for inc in (False, True):
         _check_attn(dsa, kv, mirror, batch, table, [1] * B, starts, q, 0.125, inc, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_pool_beyond_32_bit_offsets(dsa, fmt):
+    # the same pages at the start of a small pool and at the end of one whose K
+    # and V pass 2^32 bytes each: bit-identical results and cache contents
+    g = _gen(31)
+    page, n_kv, n_h, D, lens = 128, 16, 32, 128, [300, 1, 140]
+    n = sum(-(-x // page) for x in lens)
+    big = (1 << 32) // (page * n_kv * D * (2 if fmt == "bf16" else 1)) + 2 * n
+    k, v, q = (_bf16(g, sum(lens), h, D).cuda() for h in (n_kv, n_kv, n_h))
+    kept = []
+    for n_pages, first in ((n, 0), (big, big - n)):
+        kv = dsa.PagedKV.empty(n_pages, page, n_kv, D, fmt=fmt)
+        t = torch.full((3, 3), -1, dtype=torch.int32)
+        at = first
+        for b, x in enumerate(lens):
+            t[b, :-(-x // page)] = torch.arange(at, at + -(-x // page))
+            at += -(-x // page)
+        batch = dsa.PagedBatch.from_lens(lens, [0] * 3, t.cuda())
+        for name in ("k", "v"):
+            getattr(kv, name).view(torch.uint8)[first:first + n].zero_()
+        dsa.paged_append(kv, batch, k, v)
+        assert dsa.check_paged(kv, batch) == 0
+        rows = dsa.PagedBatch.from_lens([1, 1, 1], [299, 0, 139], t.cuda())
+        sel = dsa.page_topk(q[:3], kv, rows, 2, inclusive=True)
+        kept.append([dsa.paged_attn(q, kv, batch, 0.09, inclusive=True), dsa.paged_attn(q[:3], kv, rows, 0.09, inclusive=True), sel,
+                     dsa.paged_attn(q[:3], kv, rows, 0.09, sel=sel, inclusive=True)] +
+                    [getattr(kv, x).view(torch.uint8)[first:first + n].clone() for x in ("k", "v")])
+        dsa.check_device_errors()
+        del kv
+    for a, b in zip(*kept):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_a_captured_decode_step_follows_its_inputs(dsa, fmt):
+    # append, selection and attention captured once and replayed with new rows
+    # and positions give what eager calls give on a copy of the cache
+    g = _gen(32)
+    starts, page, n_kv, n_h, D, steps = [200, 37, 63], 64, 2, 8, 64, 4
+    room = [s + steps + 1 for s in starts]
+    table, t, n_pages = _table(room, [0] * 3, page, g)
+    caches = [_pool(dsa, n_pages, page, n_kv, D, fmt) for _ in range(2)]
+    k, v = _bf16(g, sum(starts), n_kv, D).cuda(), _bf16(g, sum(starts), n_kv, D).cuda()
+    cos, sin = (x.cuda() for x in _angles(max(room), D))
+    for kv in caches:
+        dsa.paged_append(kv, dsa.PagedBatch.from_lens(starts, [0] * 3, t), k, v, cos, sin)
+    pos = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    batch = dsa.PagedBatch(cu, pos, t, total_q=3, max_Lq=1, max_Lk=max(room))
+    x = [_bf16(g, 3, h, D).cuda() for h in (n_kv, n_kv, n_h)]
+
+    def step(kv, out):
+        qr = dsa.paged_append(kv, batch, x[0], x[1], cos, sin, q=x[2])
+        sel = dsa.page_topk(qr, kv, batch, 2, inclusive=True)
+        out[0].copy_(dsa.paged_attn(qr, kv, batch, 0.125, sel=sel, inclusive=True))
+        out[1].copy_(dsa.paged_attn(qr, kv, batch, 0.125, inclusive=True))
+
+    outs = [[torch.empty((3, n_h, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step(caches[0], outs[0])
+        for i in range(steps):
+            for y in x:
+                y.copy_(_bf16(g, *y.shape, std=1.0 + i))
+            graph.replay()
+            step(caches[1], outs[1])
+            s.synchronize()
+            for a, b in zip(*outs):
+                assert torch.equal(a, b)
+            for name in ("k", "v", "k_scale", "sum", "sum_scale"):
+                if getattr(caches[0], name) is not None:
+                    assert torch.equal(*(getattr(c, name).view(torch.uint8) for c in caches)), name
+            pos += 1
+    dsa.check_device_errors()
