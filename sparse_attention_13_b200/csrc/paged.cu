@@ -86,8 +86,8 @@ __device__ __forceinline__ void rotate8(const uint4& raw, int vec, int pos, cons
   const bool turn = c < 2 * p.half;
   if (p.interleaved) {
     if (!turn) return;
-    const float4 cs = __ldg(reinterpret_cast<const float4*>(p.cos + at + c / 2));
-    const float4 sn = __ldg(reinterpret_cast<const float4*>(p.sin + at + c / 2));
+    const float4 cs = ld_global(reinterpret_cast<const float4*>(p.cos + at + c / 2));
+    const float4 sn = ld_global(reinterpret_cast<const float4*>(p.sin + at + c / 2));
     const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -110,7 +110,7 @@ __device__ __forceinline__ void rotate8(const uint4& raw, int vec, int pos, cons
   const int pair = low ? c : c - p.half;
   const float4* cs4 = reinterpret_cast<const float4*>(p.cos + at + pair);
   const float4* sn4 = reinterpret_cast<const float4*>(p.sin + at + pair);
-  const float4 c0 = __ldg(cs4), c1 = __ldg(cs4 + 1), s0 = __ldg(sn4), s1 = __ldg(sn4 + 1);
+  const float4 c0 = ld_global(cs4), c1 = ld_global(cs4 + 1), s0 = ld_global(sn4), s1 = ld_global(sn4 + 1);
   const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
   const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
@@ -145,7 +145,7 @@ __device__ __forceinline__ float block_max(float x, float* red) {
 // 8 columns of every (256 / (D/8))-th slot, in registers from the load to the
 // store.  Bound by memory for prompts (13,653 rows of 64 + 8 + 8 heads of 128,
 // 8-bit pages: 108 us, 4.9 TB/s of the bytes that have to move; 75 us of it the
-// queries) and by the chain of dependent loads for a decode step (64 rows: 7 us).
+// queries) and by the chain of dependent loads for a decode step (64 rows: 11 us).
 template <int D, int PAGE, bool F8>
 __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged_append_kernel(const AppendParams p) {
   constexpr int kVecs = D / 8;                    // threads per slot
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged
     const int64_t row = w / p.q_runs;
     if (row >= p.a.total_q) return;
     const int b = paged_seq(p.a, static_cast<int>(row));
-    const int64_t pos = static_cast<int64_t>(__ldg(p.a.sp + b)) + row - paged_first(p.a, b);
+    const int64_t pos = static_cast<int64_t>(ld_global(p.a.sp + b)) + row - paged_first(p.a, b);
     if (p.half && (pos < 0 || pos >= p.n_pos)) return;
     // the lane's two vectors: a rotating pair, or two neighbours behind the
     // rotated columns; the angles are read once for all heads
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged
       const int64_t at = pos * p.half + 8 * i;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p.cos + at) + v), y = __ldg(reinterpret_cast<const float4*>(p.sin + at) + v);
+        const float4 x = ld_global(reinterpret_cast<const float4*>(p.cos + at) + v), y = ld_global(reinterpret_cast<const float4*>(p.sin + at) + v);
         cc[4 * v] = x.x; cc[4 * v + 1] = x.y; cc[4 * v + 2] = x.z; cc[4 * v + 3] = x.w;
         ss[4 * v] = y.x; ss[4 * v + 1] = y.y; ss[4 * v + 2] = y.z; ss[4 * v + 3] = y.w;
       }
@@ -241,14 +241,14 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged
     const bool some = paged_block(p.a, u, [&](int s) {
       int r, rows;
       paged_rows(p.a, s, r, rows);
-      const int at = max(__ldg(p.a.sp + s), 0) % PAGE;
+      const int at = max(ld_global(p.a.sp + s), 0) % PAGE;
       return rows ? (at + rows - 1) / PAGE + 1 : 0;
     }, b, tp);
     if (!some) return;
   }
   int r0, n;
   paged_rows(p.a, b, r0, n);
-  const int sp = __ldg(p.a.sp + b);
+  const int sp = ld_global(p.a.sp + b);
   if (n == 0 || sp < 0 || static_cast<long long>(sp) + n > p.a.max_Lk) return;
   const int j = sp / PAGE + tp;              // page of the sequence
   const int first = max(sp, j * PAGE), end = min(sp + n, (j + 1) * PAGE);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kAppendThreads, PAGE * D > 8192 ? 2 : 3) paged
     raw[s] = make_uint4(0, 0, 0, 0);
     if (slot >= a0 && slot < a1) {
       const int64_t row = r0 + (j * PAGE + slot - sp);
-      raw[s] = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) + head * D + c));
+      raw[s] = ld_global(reinterpret_cast<const uint4*>((is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) + head * D + c));
     }
   }
   float f[kSteps][8];
@@ -420,7 +420,7 @@ __device__ __forceinline__ void pooled_query(const SelParams& p, int64_t row, in
   for (int h = 0; h < G; ++h)
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(x + h * D) + i);
+      const uint32_t w = ld_global(reinterpret_cast<const uint32_t*>(x + h * D) + i);
       acc[2 * i] += static_cast<double>(__uint_as_float(w << 16));
       acc[2 * i + 1] += static_cast<double>(__uint_as_float(w & 0xffff0000u));
     }
@@ -443,8 +443,8 @@ __device__ __forceinline__ void pooled_query(const SelParams& p, int64_t row, in
 template <int D>
 __device__ __forceinline__ void load_summary(const PagedArgs& a, int64_t unit, int4 (&s)[D / 16], float& scale) {
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) s[i] = __ldg(reinterpret_cast<const int4*>(a.sum + unit * D) + i);
-  scale = __ldg(a.sum_scale + unit);
+  for (int i = 0; i < D / 16; ++i) s[i] = ld_global(reinterpret_cast<const int4*>(a.sum + unit * D) + i);
+  scale = ld_global(a.sum_scale + unit);
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
       scale[e] = 0.f;
       if (pg[e] >= 0) {
         const int64_t unit = static_cast<int64_t>(pg[e]) * p.a.n_kv + head;
-        w[e] = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D) + lane % kLanes);
-        scale[e] = __ldg(p.a.sum_scale + unit);
+        w[e] = ld_global(reinterpret_cast<const int4*>(p.a.sum + unit * D) + lane % kLanes);
+        scale[e] = ld_global(p.a.sum_scale + unit);
       }
     }
 #pragma unroll
@@ -726,8 +726,8 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
         const int j = j0 + g + 8 * e, pg = j < n_max ? paged_page(p.a, b, j) : -1;
         const int64_t unit = static_cast<int64_t>(max(pg, 0)) * p.a.n_kv + head;
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) s[e][v] = __ldg(reinterpret_cast<const int4*>(p.a.sum + unit * D + v * 64) + tq);
-        scale[e] = pg >= 0 ? __ldg(p.a.sum_scale + unit) : 0.f;
+        for (int v = 0; v < kVecs; ++v) s[e][v] = ld_global(reinterpret_cast<const int4*>(p.a.sum + unit * D + v * 64) + tq);
+        scale[e] = pg >= 0 ? ld_global(p.a.sum_scale + unit) : 0.f;
       }
       int d[4] = {0, 0, 0, 0};
 #pragma unroll

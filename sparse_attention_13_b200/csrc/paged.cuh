@@ -21,12 +21,20 @@ struct PagedArgs {
   bool one;  // every sequence has one row (the contract then fixes cu_q: no loads for it)
 };
 
+// Loads of what earlier work in the stream wrote.  Not read-only loads: the
+// kernels start before that work ends (programmatic dependent launch), and a
+// read-only load may be moved ahead of the wait for it, or hit a stale line.
+template <typename T>
+__device__ __forceinline__ T ld_global(const T* p) {
+  return *p;
+}
+
 // Row range of sequence b, clamped so that a batch that breaks its contract
 // still names only rows of the tensors.
 __device__ __forceinline__ void paged_rows(const PagedArgs& a, int b, int& r0, int& n) {
   if (a.one) { r0 = b; n = 1; return; }
-  r0 = min(max(__ldg(a.cu_q + b), 0), a.total_q);
-  n = min(max(__ldg(a.cu_q + b + 1) - r0, 0), min(a.max_Lq, a.total_q - r0));
+  r0 = min(max(ld_global(a.cu_q + b), 0), a.total_q);
+  n = min(max(ld_global(a.cu_q + b + 1) - r0, 0), min(a.max_Lq, a.total_q - r0));
 }
 
 // Sequence of a packed row: the last b with cu_q[b] <= row.
@@ -35,24 +43,24 @@ __device__ __forceinline__ int paged_seq(const PagedArgs& a, int row) {
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.cu_q + mid) <= row) lo = mid; else hi = mid - 1;
+    if (ld_global(a.cu_q + mid) <= row) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
 // First packed row of sequence b.
-__device__ __forceinline__ int paged_first(const PagedArgs& a, int b) { return a.one ? b : __ldg(a.cu_q + b); }
+__device__ __forceinline__ int paged_first(const PagedArgs& a, int b) { return a.one ? b : ld_global(a.cu_q + b); }
 
 // Positions visible to the row: s < start_pos + i (+ 1 when inclusive).
 __device__ __forceinline__ int paged_visible(const PagedArgs& a, int b, int i, int inclusive) {
-  const long long t = static_cast<long long>(__ldg(a.sp + b)) + i + inclusive;
+  const long long t = static_cast<long long>(ld_global(a.sp + b)) + i + inclusive;
   return static_cast<int>(t < 0 ? 0 : (t > a.max_Lk ? a.max_Lk : t));
 }
 
 // Pool page of page j of sequence b, or -1 when there is none.
 __device__ __forceinline__ int paged_page(const PagedArgs& a, int b, int j) {
   if (j < 0 || j >= a.max_pages) return -1;
-  const int p = __ldg(a.bt + static_cast<int64_t>(b) * a.max_pages + j);
+  const int p = ld_global(a.bt + static_cast<int64_t>(b) * a.max_pages + j);
   return p >= 0 && p < a.n_pages ? p : -1;
 }
 

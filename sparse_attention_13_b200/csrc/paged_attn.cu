@@ -155,7 +155,7 @@ struct Walker {
       s.row0 = at;
       if (b < 0) b = paged_seq(p.a, at);
       else if (p.a.one) b = at;
-      else while (b + 1 < p.a.B && __ldg(p.a.cu_q + b + 1) <= at) ++b;
+      else while (b + 1 < p.a.B && ld_global(p.a.cu_q + b + 1) <= at) ++b;
       s.nr = 1;
       s.t0 = s.t1 = paged_visible(p.a, b, at - paged_first(p.a, b), p.inclusive);
     } else {
@@ -202,7 +202,7 @@ struct Walker {
         int l0 = (p.n_sel - 1) / 32 * 32, last = -1;
         for (; l0 >= 0 && last < 0; l0 -= 32) {
           const int l = l0 + (static_cast<int>(threadIdx.x) & 31);
-          const int e = l < p.n_sel ? __ldg(list + l) : -1;
+          const int e = l < p.n_sel ? ld_global(list + l) : -1;
           const unsigned m = __ballot_sync(0xffffffffu, e >= 0 && e < n_vis);
           if (m) last = l0 + 31 - __clz(m);
         }
@@ -330,13 +330,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const int n_vis = (g.t1 + p.page - 1) >> p.shift, n_list = SPARSE ? p.n_sel : n_vis;
       const int l = tile0 * p.ppt + lane;
       j = -1;
-      if (l < n_list) j = SPARSE ? __ldg(p.sel + (static_cast<int64_t>(g.row0) * p.a.n_kv + g.kvh) * p.n_sel + l) : l;
+      if (l < n_list) j = SPARSE ? ld_global(p.sel + (static_cast<int64_t>(g.row0) * p.a.n_kv + g.kvh) * p.n_sel + l) : l;
       pg = j >= 0 && j < n_vis ? paged_page(p.a, g.b, j) : -1;
       ks = vs = 0.f;
       if (F8 && pg >= 0) {
         const int64_t u = static_cast<int64_t>(pg) * p.a.n_kv + g.kvh;
-        ks = __ldg(p.a.k_scale + u);
-        vs = __ldg(p.a.v_scale + u);
+        ks = ld_global(p.a.k_scale + u);
+        vs = ld_global(p.a.v_scale + u);
       }
     };
     int j, pg, jn, pn, j2, p2;
@@ -467,7 +467,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         qw[e] = make_uint4(0, 0, 0, 0);
         if (n < g.nh) {
           const int r = SPARSE ? 0 : n / heads;
-          qw[e] = __ldg(reinterpret_cast<const uint4*>(
+          qw[e] = ld_global(reinterpret_cast<const uint4*>(
               p.q + (static_cast<int64_t>(g.row0 + r) * p.n_h + g.kvh * p.G + g.h0 + (n - r * heads)) * D + vec * 8));
         }
       }

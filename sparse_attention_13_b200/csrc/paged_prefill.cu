@@ -259,8 +259,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       ks = vs = 1.f;
       if (F8 && pg >= 0) {
         const int64_t at = static_cast<int64_t>(pg) * p.a.n_kv + u.kvh;
-        ks = __ldg(p.a.k_scale + at);
-        vs = __ldg(p.a.v_scale + at);
+        ks = ld_global(p.a.k_scale + at);
+        vs = ld_global(p.a.v_scale + at);
       }
     };
     float vmax = -INFINITY;  // largest log2 of a V scale so far
@@ -489,7 +489,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         float amax = 0.f;
         for (int c = 0; c < D / 8; ++c) {
           float f[8];
-          bf16x8_to_f32(live ? __ldg(src + c) : make_uint4(0, 0, 0, 0), f);
+          bf16x8_to_f32(live ? ld_global(src + c) : make_uint4(0, 0, 0, 0), f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
         }
@@ -499,7 +499,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         cr *= __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
       }
       for (int c = 0; c < D / 8; ++c) {
-        uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+        uint4 w = live ? ld_global(src + c) : make_uint4(0, 0, 0, 0);
         if constexpr (F8) {
           float f[8];
           bf16x8_to_f32(w, f);
