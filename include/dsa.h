@@ -355,7 +355,9 @@ dsa_status dsa_paged_append(const dsa_paged_kv *kv, const dsa_paged_batch *batch
  * are always selected (n_last >= 1: the last page may be incomplete and has no
  * summary then; n_first + n_last <= n_sel).  Output sel [total_q, n_kv, n_sel]
  * int32: page numbers within the sequence, ascending, then -1; equal scores
- * prefer the lower page; all pages when n <= n_sel.  A row that sees nothing
+ * prefer the lower page; all pages when n <= n_sel.  A score beyond f32's range
+ * counts as the largest (or lowest) finite one, and one that is not a number
+ * (a summary that no call wrote) as the lowest.  A row that sees nothing
  * gets -1.  A pooled query that is not finite, or
  * below 3.8e-37 everywhere, scores 0 on every page.
  * Supported: n_sel <= 1024, n_h / n_kv <= 128, ceil(max_Lk / page) <= 49152. */

@@ -676,6 +676,12 @@ __device__ __forceinline__ void mma_s8_16x8x32(int (&d)[4], uint32_t a0, uint32_
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A page's score.  Only finite ones, so that a product beyond f32's range or a
+// summary that no call wrote (NaN: the lowest) never looks like a forced page.
+__device__ __forceinline__ float page_score(int dot, float scale) {
+  return fminf(fmaxf(__fmul_rn(static_cast<float>(dot), scale), -kMaxF32), kMaxF32);
+}
+
 // Many rows: one block per (eight rows of a sequence, head).  The scores of
 // eight rows and sixteen pages are one small integer matrix product, with the
 // columns permuted so that a lane's operands are 16 consecutive bytes; then a
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = j0 + g + 8 * (e >> 1), c = e & 1;
-        const float x = __fmul_rn(static_cast<float>(d[e]), scale[e >> 1]);
+        const float x = page_score(d[e], scale[e >> 1]);
         if (j < n_max) score[(2 * tq + c) * p.key_stride + j] = j >= p.n_first && j < last[c] ? x : INFINITY;
       }
     }
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
   int above = 0, forced = p.n_first + p.n_last;
   bool done = forced >= p.n_sel, exact = done;
   const float gain = kRowBins / (v_hi - v_lo), off = -v_lo * gain;
-  if (!done && v_hi > v_lo && gain < 1e30f && fabsf(off) < 1e30f) {
+  if (!done && v_hi > v_lo && gain > 0.f && gain < 1e30f && fabsf(off) < 1e30f) {
     // equal steps of value (forced pages in the last one): the step that holds
     // the n_sel-th largest score, and its scores (up to 32) ranked
     int* h = hist[warp];
@@ -879,7 +885,7 @@ __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelPa
       if (lane >= o) csum += y;
     }
     int to = at + csum - cnt;
-    while (bits) {
+    while (bits && to < p.n_sel) {  // (n_sel in all: a bound, not a case)
       out[to++] = base + lane * 32 + __ffs(bits) - 1;
       bits &= bits - 1;
     }
