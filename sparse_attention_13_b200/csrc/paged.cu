@@ -460,6 +460,12 @@ __device__ __forceinline__ uint32_t key_between(uint32_t lo, uint32_t hi, int st
   return mid;
 }
 
+// A page's score.  Only finite ones, so that a product beyond f32's range or a
+// summary that no call wrote (NaN: the lowest) never looks like a forced page.
+__device__ __forceinline__ float page_score(int dot, float scale) {
+  return fminf(fmaxf(__fmul_rn(static_cast<float>(dot), scale), -kMaxF32), kMaxF32);
+}
+
 constexpr uint32_t kForced = 0xffffffffu;  // above the key of every finite score
 
 // Decode rows: one cluster per (row, head).  Each block scores a part of the
@@ -531,7 +537,7 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
       for (int o = kLanes / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       const bool scored = j >= p.n_first && j < n - p.n_last;
       // (a page outside the pool leaves the zeros: score 0)
-      const uint32_t key = scored ? float_key(__fmul_rn(static_cast<float>(dot), scale[e])) : kForced;
+      const uint32_t key = scored ? float_key(page_score(dot, scale[e])) : kForced;
       if (j < j1 && lane % kLanes == 0) asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dst + 4u * j), "r"(key) : "memory");
     }
   }
@@ -552,7 +558,7 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
   low = __reduce_min_sync(0xffffffffu, low);
   high = __reduce_max_sync(0xffffffffu, high);
   if (lane == 0) { red[0][warp] = low; red[1][warp] = high; }
-  if (tid == 0) pick[0] = -1;
+  if (tid < 4) pick[tid] = 0;
   __syncthreads();
   low = __reduce_min_sync(0xffffffffu, red[0][lane % kDecWarps]);
   high = __reduce_max_sync(0xffffffffu, red[1][lane % kDecWarps]);
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
   bool exact = above >= p.n_sel;  // exactly the keys >= low are taken
   if (exact) low = kForced;       // the forced pages alone
   const float v0 = key_value(low), gain = kBins / (key_value(high) - v0);
-  if (!exact && high > low && gain < 1e30f) {
+  if (!exact && high > low && gain > 0.f && gain < 1e30f) {
     const auto bin = [&](uint32_t key) { return min(kBins - 1, static_cast<int>((key_value(key) - v0) * gain)); };  // grows with the value
     for (int i = 0; i < per; ++i) {
       const uint32_t x = w0 + i * 32 < n ? keys[w0 + i * 32] : kForced;
@@ -662,8 +668,8 @@ __global__ void __launch_bounds__(kDecThreads) page_topk_kernel(const SelParams 
     const bool gt = is_gt(i, eq);
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     const int g0 = at + __popc(bg & lt), e0 = ties + __popc(be & lt);
-    if (gt) out[g0 + min(e0, want)] = w0 + i * 32;
-    else if (eq && e0 < want) out[g0 + e0] = w0 + i * 32;
+    const int to = g0 + min(e0, want);
+    if ((gt || (eq && e0 < want)) && to < p.n_sel) out[to] = w0 + i * 32;  // (n_sel in all: a bound, not a case)
     at += __popc(bg);
     ties += __popc(be);
   }
@@ -674,12 +680,6 @@ __device__ __forceinline__ void mma_s8_16x8x32(int (&d)[4], uint32_t a0, uint32_
   asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// A page's score.  Only finite ones, so that a product beyond f32's range or a
-// summary that no call wrote (NaN: the lowest) never looks like a forced page.
-__device__ __forceinline__ float page_score(int dot, float scale) {
-  return fminf(fmaxf(__fmul_rn(static_cast<float>(dot), scale), -kMaxF32), kMaxF32);
 }
 
 // Many rows: one block per (eight rows of a sequence, head).  The scores of

@@ -78,3 +78,76 @@ def test_selection_of_a_chunk_with_scales_that_no_call_wrote(dsa, share, value):
     kv.sum_scale[torch.rand(kv.sum_scale.shape, generator=g).cuda() < share] = value
     kv.sum[::5] = 0  # (a dot product of 0 times infinity)
     _check_selection(dsa, kv, batch, table, q_lens, starts, _bf16(g, 13, 4, 64), 16)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens", [400, 8000, 40000])
+def test_selection_of_few_rows_with_infinite_scores(dsa, tokens, fmt):  # noqa: F811
+    q_lens, starts = [1, 3], [tokens, tokens // 2]
+    kv, mirror, batch, table, g = _filled(dsa, q_lens, starts, 2, 128, 16, fmt, 43, hook=_huge_keys(16))
+    q = _bf16(g, 4, 8, 128) + 0.5
+    _check_selection(dsa, kv, batch, table, q_lens, starts, q, 16)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("share", [0.1, 0.98, 1.0])
+@pytest.mark.parametrize("tokens", [500, 40000])
+def test_selection_of_few_rows_with_scales_that_no_call_wrote(dsa, tokens, share, value):  # noqa: F811
+    q_lens, starts = [1, 1, 1], [tokens, 500, 130]
+    kv, mirror, batch, table, g = _filled(dsa, q_lens, starts, 2, 64, 16, "bf16", 44)
+    kv.sum_scale[torch.rand(kv.sum_scale.shape, generator=g).cuda() < share] = value
+    kv.sum[::5] = 0
+    _check_selection(dsa, kv, batch, table, q_lens, starts, _bf16(g, 3, 4, 64), 16)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [6, 5]])
+def test_selection_where_the_positions_run_ahead_of_the_cache(dsa, q_lens):  # noqa: F811
+    # a first position beyond the appended tokens breaks the contract: the rows
+    # are unspecified, but lists name visible pages and end where they should
+    g, page, n_sel = _gen(45), 16, 8
+    table, t, n_pages = _table([400, 400], [0, 0], page, g)
+    kv = _pool(dsa, n_pages, page, 2, 64, "bf16")
+    k = _bf16(g, 300, 2, 64).cuda()
+    dsa.paged_append(kv, dsa.PagedBatch.from_lens([150, 150], [0, 0], t), k, k)
+    total = sum(q_lens)
+    batch = dsa.PagedBatch.from_lens(q_lens, [380, 300], t)
+    out, guard = _guarded((total, 2, n_sel), torch.int32, -77)
+    dsa.page_topk(_bf16(g, total, 4, 64).cuda(), kv, batch, n_sel, inclusive=True, out=out)
+    dsa.check_device_errors()
+    assert (guard == -77).all() and (out >= 0).all() and (out < 25).all()
+    assert (out[..., 1:] > out[..., :-1]).all()
+
+
+def _summaries(dsa, lens, page, n_kv, D, g):
+    """A pool that has summaries alone (codes and scales drawn), with its table."""
+    table, t, n_pages = _table(lens, [0] * len(lens), page, g, spare=1)
+    kv = dsa.PagedKV.empty(n_pages, page, n_kv, D, fmt="e4m3")
+    kv.sum.copy_(torch.randint(-127, 128, kv.sum.shape, generator=g, dtype=torch.int8))
+    kv.sum_scale.copy_(torch.rand(kv.sum_scale.shape, generator=g) + 0.5)
+    return kv, table, t
+
+
+@pytest.mark.parametrize("spread", [0, 1, 900])
+def test_selection_of_few_rows_with_crowded_scores(dsa, spread):  # noqa: F811
+    # one page scores far above the others, which crowd into one of the equal
+    # steps of value, with many or few different values among them
+    g = _gen(46)
+    kv, table, t = _summaries(dsa, [20000, 9000], 16, 2, 64, g)
+    kv.sum.fill_(3)
+    kv.sum_scale.copy_(1.0 + torch.randint(0, spread + 1, kv.sum_scale.shape, generator=g) * 2.0 ** -20)
+    for b, far in ((0, 700), (1, 33)):
+        kv.sum_scale[table[b][far]] = 1e6
+    q = _bf16(g, 2, 4, 64) + 2
+    _check_selection(dsa, kv, dsa.PagedBatch.from_lens([1, 1], [19999, 8999], t), table, [1, 1], [19999, 8999], q, 33)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,ends", [([1], [49152 * 16]), ([6, 4], [6369 * 16, 49000 * 16 - 3]), ([6], [6368 * 16])])
+def test_selection_among_the_most_pages(dsa, D, q_lens, ends):  # noqa: F811
+    # up to the most pages of a sequence; chunks on both sides of what the
+    # shared memory of the kernel for many rows holds
+    g = _gen(47)
+    kv, table, t = _summaries(dsa, ends, 16, 1, D, g)
+    starts = [e - n for e, n in zip(ends, q_lens)]
+    q = _bf16(g, sum(q_lens), 3, D)
+    _check_selection(dsa, kv, dsa.PagedBatch.from_lens(q_lens, starts, t), table, q_lens, starts, q, 100)
