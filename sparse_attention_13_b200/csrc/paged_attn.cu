@@ -986,7 +986,7 @@ dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, co
     x.out = out; x.lse = lse; x.err = err;
     if (pl.splits > 1) {
       x.part_o = reinterpret_cast<float*>(w);
-      x.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
+      x.part_l = reinterpret_cast<float2*>(w + pl.o_bytes);
     }
     e = paged_prefill_launch(mk, mv, kv->D, f8, x, s);
   } else {

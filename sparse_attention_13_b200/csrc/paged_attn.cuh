@@ -16,7 +16,8 @@ struct PrefillParams {
   float scale_log2;
   dsa_bf16* out;
   float* lse;
-  float *part_o, *part_l;                   // [unit][split][2][128] (x D)
+  float* part_o;                            // [unit][split][2][128][D]
+  float2* part_l;                           // [unit][split][2][128]: log2 of a part's sum is x + y
   unsigned int* err;
 };
 

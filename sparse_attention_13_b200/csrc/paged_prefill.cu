@@ -36,6 +36,12 @@ constexpr int kSoftRegs = 208, kOtherRegs = 48;
 // more than this (f16 holds 2^16): rescaling O is rare, and no maximum is taken
 // on the way.
 constexpr float kMostSum = 4096.f;
+// A score is rounded to f32 before it becomes the reference, but not inside the
+// fused exponent score * k - reference.  Up to this reference the difference is
+// at most 2^-8; beyond, the exponent takes the rounded score as well (at 2^28
+// the difference is 16, and a weight of 2^16 after its own maximum), and the
+// share of the V scales, which such a sum would swallow, is kept apart (off).
+constexpr float kFarRef = 65536.f;
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -118,6 +124,86 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int 
       sum = F8 ? fmaf(part, inv, sum) : sum + part;
     }
   }
+}
+
+// O follows a new reference.
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t to, float f) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32<32>(to + c * 32, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tmem_st32x32(to + c * 32, o);
+  }
+  tmem_st_wait();
+}
+
+// A row's state: reference exponent (ref + off; off is zero up to kFarRef) and
+// the sum of 2^(score - reference).
+struct RowState {
+  float ref, off, l;
+};
+
+// Half a tile of rows whose scores are past kFarRef: maxima, O (the product of
+// the half before has been added), weights (stored over the scores) and sum.
+// Apart from tile_weights, whose ordinary halves it would slow down by 2 %.
+template <int D, bool F8>
+__device__ __forceinline__ RowState far_half(uint32_t ts, uint32_t to, const float4* mt, int shift, float cr, int lim, bool first, RowState row) {
+  const auto scales = [&](int r) { return F8 ? mt[r * 16 >> shift] : make_float4(1.f, 0.f, 1.f, 0.f); };
+  const auto load = [&](int r, float (&x)[16]) {  // scores of a run of 16 keys
+    uint32_t s[16];
+    tmem_ld32<16>(ts + r * 16, s);
+    tmem_ld_wait();
+    const float k = F8 ? cr * scales(r).x : cr;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = r * 16 + e < lim ? __fmul_rn(__uint_as_float(s[e]), k) : -INFINITY;
+  };
+  float x[16];
+  // the largest bare score is the base, what the V scales add comes on top
+  float next = row.ref;
+#pragma unroll 1
+  for (int r = 0; r < 4; ++r) {
+    load(r, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) next = fmaxf(next, x[e]);
+  }
+  const float was = row.ref == next ? row.off : row.off + (row.ref - next);  // the reference so far, from the new base
+  const float mu = next == -INFINITY ? 0.f : next;
+  float off = was;
+#pragma unroll 1
+  for (int r = 0; r < 4; ++r) {
+    load(r, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) off = fmaxf(off, __fadd_rn(__fsub_rn(x[e], mu), scales(r).y));
+  }
+  const float f = off == was ? 1.f : ex2_approx(was - off);
+  if (!first && __any_sync(0xffffffffu, f != 1.f)) scale_o<D>(to, f);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int r = 0; r < 4; ++r) {  // (the weights of a run lie over scores that have been read)
+    uint32_t pk[8];
+    load(r, x);
+    const float4 sc = scales(r);
+    const bool thin = sc.w == 1.f || sc.w == 3.f;
+    float part = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float d = __fsub_rn(x[e + i], mu);
+        w[i] = ex2_approx(d + (sc.y - off));
+        part += thin ? ex2_approx(d - off) : w[i];
+      }
+      pk[e / 2] = F8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]);
+    }
+    sum = fmaf(part, thin ? 1.f : sc.z, sum);
+    tmem_st32x8(ts + r * 8, pk);
+  }
+  return {next, off, fmaf(row.l, f, sum)};
 }
 
 template <int D, bool F8>
@@ -514,10 +600,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       if (lane == 0) mbar_arrive(q_full);
     }
 
-    float ref = -INFINITY, l = 0.f;  // reference exponent, sum of 2^(score - ref)
+    float ref = -INFINITY, off = 0.f, l = 0.f;
     const int nt = q ? (u.nq > 1 ? n_tiles : 0) : n0;
     bool ok = true;
     bool thin = false;  // a page of the tile has a V scale far below the others'
+    bool far = false;   // a row's reference is past kFarRef
     for (int g = 0; g < 2 * nt && ok; ++g) {
       const int i = g >> 1, h = g & 1;
       const int lim = t - (u.lo + i) * kTile - h * kHalf;  // keys of the half that the row sees
@@ -533,7 +620,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
       bool find = g == 0;  // (a row that sees no key of the first half sees none)
       uint32_t pk[32];
       float sum;
-      while (true) {
+      for (int tries = 0; !far; tries = 1) {
         if (find) {  // the rows' maxima first
           float top = -INFINITY;
 #pragma unroll
@@ -556,33 +643,37 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
           }
           const float next = fmaxf(ref, top);
+          far = __any_sync(0xffffffffu, fabsf(next) > kFarRef && next != -INFINITY);
+          if (far) break;
           const float f = next == ref ? 1.f : ex2_approx(ref - next);
           ref = next;
           l *= f;
           if (g > 0 && __any_sync(0xffffffffu, f != 1.f)) {  // once the product of the half before has been added
             ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[2 * q + (h ^ 1)], ((g - 1) >> 1) & 1, abort_flag));
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32<32>(to + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32x32(to + c * 32, o);
-            }
-            tmem_st_wait();
+            scale_o<D>(to, f);
           }
         }
-        const float mu = ref == -INFINITY ? 0.f : ref;
+        // (all scores so far -inf: the first one that is not asks for the maxima)
+        const float mu = ref == -INFINITY ? -1e38f : ref;
         float high;
         if (edge || thin) tile_weights<F8, true>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
         else tile_weights<F8, false>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
-        if (!__any_sync(0xffffffffu, high > kMostSum)) break;
+        // (once the maxima have been taken no exponent is above 2^-8: one more try at most)
+        if (tries || !__any_sync(0xffffffffu, high > kMostSum)) break;
         find = true;
       }
-      l += sum;
-      tmem_st32x32(th, pk);
+      if (far) {
+        if (g > 0) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[2 * q + (h ^ 1)], ((g - 1) >> 1) & 1, abort_flag));
+        tc_fence_after();
+        const RowState row = far_half<D, F8>(th, to, mt, p.shift, cr, lim, g == 0, {ref, off, l});
+        ref = row.ref;
+        off = row.off;
+        l = row.l;
+      } else {
+        l += sum;
+        tmem_st32x32(th, pk);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -594,7 +685,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     if (ok && q < u.nq) {
       tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float l2 = l == 0.f ? -INFINITY : ref + log2f(l);
+      const float ls = off + log2f(l);  // with ref: log2 of the row's sum (apart, since ref may swallow it)
       const int64_t part = ((id * p.splits + split) * 2 + q) * 128 + m;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -620,8 +711,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
       }
       if (live) {
-        if (p.splits > 1) p.part_l[part] = l2;
-        else if (p.lse) p.lse[at] = l2 == -INFINITY ? -INFINITY : l2 * 0.6931471805599453f;
+        if (p.splits > 1) p.part_l[part] = l == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(ref, ls);
+        else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (ref + ls) * 0.6931471805599453f;
         if (*poison)
           add_nonfinite<D, F8>(p, u.b, u.kvh, max(u.t0, u.lo * kTile), min(t, u.hi[1] * kTile), p.splits > 1 ? p.part_o + part * D : nullptr,
                                p.out + at * D);
@@ -653,13 +744,17 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
   const int tok = m / p.G, row = (last - blk) * 2 * p.tok + q * p.tok + tok;
   if (tok >= p.tok || row >= n) return;
   const auto at = [&](int s) { return ((id * p.splits + s) * 2 + q) * 128 + m; };
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_l[at(s)]);
+  // sums 2^(x + y) of the parts: relative to the largest x, then to the largest of all
+  float base = -INFINITY, top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) base = fmaxf(base, p.part_l[at(s)].x);
+  if (base == -INFINITY) base = 0.f;
+  const auto log_sum = [&](int s) { return p.part_l[at(s)].x - base + p.part_l[at(s)].y; };
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, log_sum(s));
   const float ref = top == -INFINITY ? 0.f : top;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   for (int s = 0; s < p.splits; ++s) {
-    const float l2 = p.part_l[at(s)], w = exp2f(l2 - ref);
+    const float l2 = log_sum(s), w = exp2f(l2 - ref);
     sum += w;
     if (l2 == -INFINITY) continue;
     const float4 o = *reinterpret_cast<const float4*>(p.part_o + at(s) * D + v * 4);
@@ -668,7 +763,7 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const PrefillP
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t o = static_cast<int64_t>(r0 + row) * p.n_h + kvh * p.G + (m - tok * p.G);
   *reinterpret_cast<uint2*>(p.out + o * D + v * 4) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (v == 0 && p.lse) p.lse[o] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+  if (v == 0 && p.lse) p.lse[o] = sum == 0.f ? -INFINITY : (base + (ref + log2f(sum))) * 0.6931471805599453f;
 }
 
 template <int D, bool F8>
@@ -699,7 +794,7 @@ PrefillPlan paged_prefill_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb
   pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, tiles / 3)));
   if (pl.splits > 1) {
     pl.o_bytes = static_cast<size_t>(units) * pl.splits * 256 * kv->D * 4;
-    pl.l_bytes = static_cast<size_t>(units) * pl.splits * 256 * 4;
+    pl.l_bytes = static_cast<size_t>(units) * pl.splits * 256 * 8;
   }
   return pl;
 }

@@ -151,3 +151,88 @@ def test_selection_among_the_most_pages(dsa, D, q_lens, ends):  # noqa: F811
     starts = [e - n for e, n in zip(ends, q_lens)]
     q = _bf16(g, sum(q_lens), 3, D)
     _check_selection(dsa, kv, dsa.PagedBatch.from_lens(q_lens, starts, t), table, q_lens, starts, q, 100)
+
+
+def _whole(g, *shape, most=8, times=1.0):
+    """Whole numbers from -most to most, times a power of two: exact in bf16, in
+    E4M3 with a power-of-two scale, and in f32 sums of their products."""
+    return (torch.randint(-most, most + 1, shape, generator=g).double() * times).to(torch.bfloat16)
+
+
+def _check_one_hot(dsa, kv, mirror, batch, table, q_lens, starts, q, scale, sel=None):
+    """Scores so far apart that the softmax is exactly uniform over the keys
+    that share the largest one: out is the mean of their values.
+
+    Tolerance: the weights of equal scores are equal, each rounded to 8
+    significant bits as their common value (2^-8), f32 sums, and one rounding of
+    the output to bf16 (2^-8): 2^-7 of the mean of |v|, in all."""
+    n_h, n_kv, page = q.shape[1], kv.k.shape[1], kv.k.shape[2]
+    G = n_h // n_kv
+    total = sum(q_lens)
+    lse, guard = _guarded((total, n_h), torch.float32, -77.0)
+    out = dsa.paged_attn(q.cuda(), kv, batch, scale, sel=None if sel is None else sel.cuda(), inclusive=True, lse=lse)
+    dsa.check_device_errors()
+    out, lse, r = out.cpu().double(), lse.cpu().double(), 0
+    for b, n in enumerate(q_lens):
+        for h in range(n_kv):
+            K, V = mirror.rows(table[b], h)
+            for i in range(n):
+                t = starts[b] + i + 1
+                seen = torch.arange(K.shape[0]) < t
+                if sel is not None:
+                    chosen = torch.zeros(K.shape[0] // page, dtype=torch.bool)
+                    chosen[sel[r + i, h].long()] = True
+                    seen &= chosen.repeat_interleave(page)
+                idx = torch.nonzero(seen).flatten()
+                for x in range(G):
+                    e = K[idx] @ q[r + i, h * G + x].double()
+                    top = e.max()
+                    ties = idx[e == top]
+                    want, size = V[ties].mean(0), V[ties].abs().mean(0)
+                    err = (out[r + i, h * G + x] - want).abs()
+                    assert (err <= 2.0 ** -7 * size + 1e-30).all(), (b, i, h, x, float(err.max()), float(size.max()))
+                    want_lse = scale * float(top) + math.log(len(ties))
+                    assert abs(float(lse[r + i, h * G + x]) - want_lse) <= 2.0 ** -20 * abs(want_lse)
+        r += n
+
+
+def _equal_far_keys(dsa, q_lens, starts, D, page, fmt, times, seed):
+    """Keys of whole numbers that repeat every 97 tokens, so that a row's largest
+    score has ties in many pages, and values whose size differs between pages."""
+    def hook(k, v):
+        k.copy_(_whole(_gen(seed), 97, *k.shape[1:], times=times)[torch.arange(k.shape[0]) % 97])
+        v.mul_((2.0 ** (torch.arange(v.shape[0]) // page * 3 % 7 - 3))[:, None, None].to(v.dtype))
+    kv, mirror, batch, table, g = _filled(dsa, q_lens, starts, 2, D, page, fmt, seed + 1, hook=hook)
+    return kv, mirror, batch, table, _whole(g, sum(q_lens), 8, D, times=times)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,page,q_lens,starts", [(64, 64, [140, 70], [300, 0]), (128, 32, [140], [3000])])
+@pytest.mark.parametrize("times,scale", [(1.0, 64.0), (2.0 ** 10, 2.0 ** 9), (2.0 ** 10, 2.0 ** 40), (1.0, 1e30)])
+def test_prompts_with_scores_past_the_f32_fraction(dsa, times, scale, D, page, q_lens, starts, fmt):  # noqa: F811
+    # scores of 2^29 to 1e34: rounding one moves it by more than a weight's range
+    kv, mirror, batch, table, q = _equal_far_keys(dsa, q_lens, starts, D, page, fmt, times, 51)
+    _check_one_hot(dsa, kv, mirror, batch, table, q_lens, starts, q, scale)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq", [1, 4, 140])
+def test_keys_whose_scores_are_minus_infinity(dsa, lq, fmt):  # noqa: F811
+    # the first 192 keys have scores below the f32 range, the others lie around
+    # -3,000: the softmax is that of the others
+    def hook(k, v):
+        k[:192] = -(2.0 ** 100)
+        k[192:] = (k[192:].float() * 0.1 - 23.0).to(k.dtype) * 2.0 ** -100
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [500], 2, 128, 64, fmt, 53, hook=hook)
+    q = (torch.ones(lq, 8, 128) * 2.0 ** 100).to(torch.bfloat16)
+    lse = torch.empty((lq, 8), dtype=torch.float32, device="cuda")
+    out = dsa.paged_attn(q.cuda(), kv, batch, 1.0, inclusive=True, lse=lse).cpu().double()
+    dsa.check_device_errors()
+    for h in range(2):
+        K, V = mirror.rows(table[0], h)
+        for i in {0, lq // 2, lq - 1}:
+            seen = (torch.arange(K.shape[0]) >= 192) & (torch.arange(K.shape[0]) <= 500 + i)
+            for x in range(4):
+                want, want_lse, tol, tol_lse = ref.attend_row(q[i, h * 4 + x].double(), K, V, seen, 1.0)
+                assert ((out[i, h * 4 + x] - want).abs() <= tol).all()
+                assert abs(float(lse[i, h * 4 + x]) - want_lse) <= tol_lse
