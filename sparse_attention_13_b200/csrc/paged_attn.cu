@@ -146,6 +146,8 @@ struct Walker {
     }
   }
 
+  // (A run that begins past the own tiles of its unit begins with a segment that
+  // has none.  The roles pass over it, so that barriers count those with tiles.)
   __device__ __forceinline__ bool next(Seg& s) {
     if (pos >= end) return false;
     int nominal;
@@ -422,7 +424,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     };
     while (ok && walk.next(s)) {
       const int n = warp_uniform(s.hi - s.lo);
-      ok = wait_all(q_full, seg & 1) && (n == 0 || qk(it));
+      if (n == 0) continue;
+      ok = wait_all(q_full, seg & 1) && qk(it);
       for (int i = 0; ok && i < n; ++i) {
         const int t = it + i;
         if (i + 1 < n && !qk(t + 1)) { ok = false; break; }
@@ -513,13 +516,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (lane == 0) mbar_arrive(q_full);
     };
 
-    bool more = walk.next(s);
+    bool more;
+    do more = walk.next(s); while (more && s.lo == s.hi);
     if (more) {
       fetch_q(s);
       store_q(0);
-    } else if (p.part_l && threadIdx.x < NH) {
-      p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;  // no part of any unit
     }
+    // this CTA's part of the unit in which its run begins, where it has none
+    if (p.part_l && threadIdx.x < NH && !(more && s.slot == 0)) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;
     while (ok && more) {
       const Seg cur = s;
       more = walk.next(s);
@@ -724,12 +728,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
         if (lane == h) lsum[wq * NH + gh + h] = l[h];
       }
-      const bool any = cur.hi > cur.lo;
-      if (any && ok) ok = mbar_wait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
+      if (ok) ok = mbar_wait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
       // the other flag's readers (the segment before) are done: every warp has
       // delivered weights of this segment, and none begins the next one before
       // the barrier below
-      if (any && threadIdx.x == 0) poison[(seg & 1) ^ 1] = 0;
+      if (threadIdx.x == 0) poison[(seg & 1) ^ 1] = 0;
       if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
       tc_fence_after();
       float o[HG];
@@ -739,13 +742,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tmem_ld32<HG>(tmem_o + lanes + NH + gh, b);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < HG; ++h) o[h] = any ? fmaf(__uint_as_float(b[h]), F8 ? 1.f / 32 : 1.f, __uint_as_float(a[h])) : 0.f;
+        for (int h = 0; h < HG; ++h) o[h] = fmaf(__uint_as_float(b[h]), F8 ? 1.f / 32 : 1.f, __uint_as_float(a[h]));
       } else {
         uint32_t a[HG];
         tmem_ld32<HG>(tmem_o + lanes + gh, a);
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < HG; ++h) o[h] = any ? __uint_as_float(a[h]) : 0.f;
+        for (int h = 0; h < HG; ++h) o[h] = __uint_as_float(a[h]);
       }
       tc_fence_before();
       // lane h: total, 1 / total and log2 of head h

@@ -236,3 +236,59 @@ def test_keys_whose_scores_are_minus_infinity(dsa, lq, fmt):  # noqa: F811
                 want, want_lse, tol, tol_lse = ref.attend_row(q[i, h * 4 + x].double(), K, V, seen, 1.0)
                 assert ((out[i, h * 4 + x] - want).abs() <= tol).all()
                 assert abs(float(lse[i, h * 4 + x]) - want_lse) <= tol_lse
+
+
+def _attend(dsa, kv, mirror, batch, table, q_lens, starts, q, scale, sel=None, rows=None, tol=None):
+    """paged_attn (inclusive) against a plain form, with guards behind out and
+    lse.  tol(q, K, V, seen, scale, vs) -> (out, lse, their tolerances); vs: the
+    V scale of each position."""
+    tol = tol or _loose
+    n_h, D, n_kv, page = q.shape[1], q.shape[2], kv.k.shape[1], kv.k.shape[2]
+    total, G = sum(q_lens), q.shape[1] // kv.k.shape[1]
+    lse, g1 = _guarded((total, n_h), torch.float32, -77.0)
+    out, g2 = _guarded((total, n_h, D), torch.bfloat16, -77.0)
+    dsa.paged_attn(q.cuda(), kv, batch, scale, sel=None if sel is None else sel.cuda(), inclusive=True, out=out, lse=lse)
+    dsa.check_device_errors()
+    assert (g1 == -77).all() and (g2 == -77).all()
+    out, lse, r = out.cpu().double(), lse.cpu().double(), 0
+    for b, n in enumerate(q_lens):
+        for h in range(n_kv if n else 0):
+            K, V = mirror.rows(table[b], h)
+            vs = mirror.vs[torch.tensor(table[b], dtype=torch.long), h].repeat_interleave(page)
+            for i in range(n):
+                if rows is not None and r + i not in rows:
+                    continue
+                seen = torch.arange(K.shape[0]) <= starts[b] + i
+                if sel is not None:
+                    chosen = torch.zeros(K.shape[0] // page, dtype=torch.bool)
+                    lst = sel[r + i, h].long()
+                    chosen[lst[(lst >= 0) & (lst < chosen.numel())]] = True
+                    seen &= chosen.repeat_interleave(page)
+                for x in range(h * G, h * G + G):
+                    want, want_lse, tol_o, tol_l = tol(q[r + i, x].double(), K, V, seen, scale, vs)
+                    err = (out[r + i, x] - want).abs()
+                    assert (err <= tol_o).all(), (b, i, x, float((err / tol_o).max()))
+                    got = float(lse[r + i, x])
+                    assert got == want_lse if math.isinf(want_lse) else abs(got - want_lse) <= tol_l, (b, i, x, got, want_lse)
+        r += n
+
+
+def _loose(q, K, V, seen, scale, vs):
+    top = float(vs[seen].max()) if seen.any() else 0.0
+    return ref.attend_row(q, K, V, seen, scale, top if float(vs.max()) != 1.0 or float(vs.min()) != 1.0 else 0.0)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,n_sel,starts", [(16, 300, [40, 0, 5000, 700]), (64, 40, [0, 130, 63, 900])])
+def test_lists_much_longer_than_the_rows(dsa, page, n_sel, starts, fmt):  # noqa: F811
+    # most CTAs begin past the last page of the row they begin in
+    q_lens = [1] * 4
+    kv, mirror, batch, table, g = _filled(dsa, q_lens, starts, 2, 64, page, fmt, 61)
+    sel = torch.full((4, 2, n_sel), -1, dtype=torch.int32)
+    for b, s in enumerate(starts):
+        vis = s // page + 1
+        for h in range(2):
+            pick = torch.randperm(vis, generator=g)[:n_sel].int()
+            sel[b, h, :len(pick)] = pick
+    for shift in (0, 3):  # (also with holes before the entries)
+        _attend(dsa, kv, mirror, batch, table, q_lens, starts, _bf16(g, 4, 8, 64, std=1.5), 0.125, sel=sel.roll(shift, 2))
