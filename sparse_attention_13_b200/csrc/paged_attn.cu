@@ -36,7 +36,7 @@ struct PattnParams {
   dsa_bf16* out;
   float* lse;
   float* part_o;           // [2 CTAs][NH][D]
-  float* part_l;           // [2 CTAs][NH]
+  float2* part_l;          // [2 CTAs][NH]: log2 of a part's sum is x + y
   int2* meta;              // [units] first and last CTA of a split unit
   unsigned int* err;
 };
@@ -523,14 +523,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       store_q(0);
     }
     // this CTA's part of the unit in which its run begins, where it has none
-    if (p.part_l && threadIdx.x < NH && !(more && s.slot == 0)) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = -INFINITY;
+    if (p.part_l && threadIdx.x < NH && !(more && s.slot == 0)) p.part_l[2ll * blockIdx.x * NH + threadIdx.x] = make_float2(-INFINITY, 0.f);
     while (ok && more) {
       const Seg cur = s;
       more = walk.next(s);
       if (more) fetch_q(s);
       // lane h (mod HG) keeps the reference exponents of head h: m of the
-      // weights, mp of the weighted V scales; every thread its keys' sums
-      float m = -INFINITY, mp = -INFINITY, l[HG];
+      // weights, m + mr of the weighted V scales (relative, because a large m
+      // would swallow a scale's share); every thread its keys' sums
+      float m = -INFINITY, mr = -INFINITY, l[HG];
 #pragma unroll
       for (int h = 0; h < HG; ++h) l[h] = 0.f;
       const int heads = min(p.Gx, p.G - cur.h0);
@@ -559,13 +560,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           tmem_ld32<HG>(ts + NH + gh, b);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < HG; ++h) x[h] = fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])) * (ks * c[h]);
+          for (int h = 0; h < HG; ++h) x[h] = __fmul_rn(fmaf(__uint_as_float(b[h]), 1.f / 32, __uint_as_float(a[h])), ks * c[h]);
         } else {
           uint32_t a[HG];
           tmem_ld32<HG>(ts + gh, a);
           tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < HG; ++h) x[h] = __uint_as_float(a[h]) * p.scale_log2;
+          for (int h = 0; h < HG; ++h) x[h] = __fmul_rn(__uint_as_float(a[h]), p.scale_log2);
         }
         const bool edge = __any_sync(0xffffffffu, past >= 0);
         if (edge) {
@@ -593,23 +594,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int h = lane % HG;
           float t = -INFINITY, tp = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float y = w[q * (HG + 4) + h];
-            t = fmaxf(t, y);
-            if (F8) tp = fmaxf(tp, y + w[q * (HG + 4) + HG]);
+          for (int q = 0; q < 4; ++q) t = fmaxf(t, w[q * (HG + 4) + h]);
+          const float mn = fmaxf(m, ceilf(t));
+          const float mu = mn == -INFINITY ? 0.f : mn;
+          if (F8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tp = fmaxf(tp, (w[q * (HG + 4) + h] - mu) + w[q * (HG + 4) + HG]);
           }
-          const float mn = fmaxf(m, ceilf(t)), pn = F8 ? fmaxf(mp, ceilf(tp)) : mn;
-          const float mu = mn == -INFINITY ? 0.f : mn, mpu = pn == -INFINITY ? 0.f : pn;
+          const float was = mr + (m - mu), pr = F8 ? fmaxf(was, ceilf(tp)) : 0.f;
           grew_l = __any_sync(0xffffffffu, mn > m);
-          grew = F8 ? __any_sync(0xffffffffu, pn > mp) : grew_l;
+          grew = F8 ? __any_sync(0xffffffffu, pr > was) : grew_l;
           if (lane < HG) {
             bc[lane] = mu;
-            if (F8) bc[HG + lane] = ex2_approx(fminf(mu - mpu + 8.f, 120.f));
+            if (F8) bc[HG + lane] = ex2_approx(pr == -INFINITY ? 8.f : fminf(8.f - pr, 120.f));
             if (grew_l) bc[2 * HG + lane] = mn > m ? ex2_approx(m - mn) : 1.f;
-            if (F8 && grew) bc[3 * HG + lane] = pn > mp ? ex2_approx(mp - pn) : 1.f;
+            if (F8 && grew) bc[3 * HG + lane] = pr > was ? ex2_approx(was - pr) : 1.f;
           }
           m = mn;
-          mp = pn;
+          mr = pr;
           __syncwarp();
         }
         if (grew_l) {
@@ -755,16 +757,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       {
         const float* t = lsum + gh + lane % HG;
         const float sum = (t[0] + t[NH]) + (t[2 * NH] + t[3 * NH]);
-        const float ml = m == -INFINITY ? 0.f : m, mv = mp == -INFINITY ? 0.f : mp;
-        const float f = F8 ? ex2_approx(mv - ml - 8.f) : 1.f;
-        const float l2 = sum == 0.f ? -INFINITY : ml + log2f(sum);
+        const float f = F8 ? ex2_approx((mr == -INFINITY ? 0.f : mr) - 8.f) : 1.f;
         if (lane < HG) bc[lane] = sum == 0.f ? 0.f : f / sum;
         if (wq == 0 && lane < HG && gh + lane < cur.nh) {
           const int n = gh + lane, r = SPARSE ? 0 : n / heads;
           if (cur.slot < 0) {
-            if (p.lse) p.lse[static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads)] = sum == 0.f ? -INFINITY : l2 * kLn2;
+            if (p.lse) p.lse[static_cast<int64_t>(cur.row0 + r) * p.n_h + cur.kvh * p.G + cur.h0 + (n - r * heads)] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
           } else {
-            p.part_l[(2ll * blockIdx.x + cur.slot) * NH + n] = l2;
+            p.part_l[(2ll * blockIdx.x + cur.slot) * NH + n] = sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(m, log2f(sum));
           }
         }
         __syncwarp();
@@ -815,7 +815,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 // Joins the parts of a unit that several CTAs worked on: each part is its
-// normalised output and log2 of its sum.  One block per (unit, head).
+// normalised output, and its reference and log2 of its sum above that.  One block per (unit, head).
 template <int D>
 __global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p, int NH, int sparse) {
   pdl_trigger();
@@ -844,12 +844,18 @@ __global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p
   const int2 c = p.meta[unit];
   if (c.x < 0) return;
   const auto slot = [&](int i) { return static_cast<int64_t>(2 * i + (i == c.x)) * NH + n; };
-  float top = -INFINITY;
-  for (int i = c.x; i <= c.y; ++i) top = fmaxf(top, p.part_l[slot(i)]);
+  float base = -INFINITY, top = -INFINITY;  // top relative to the largest x, since that may swallow y
+  for (int i = c.x; i <= c.y; ++i) {
+    const float2 x = p.part_l[slot(i)];
+    if (x.x > base) { top += base - x.x; base = x.x; }
+    top = fmaxf(top, (x.x - base) + x.y);  // (NaN for the empty parts before the first sum: passed over)
+  }
+  if (base == -INFINITY) base = 0.f;
   const float ref = top == -INFINITY ? 0.f : top;
   float acc = 0.f, sum = 0.f;
   for (int i = c.x; i <= c.y; ++i) {
-    const float l2 = p.part_l[slot(i)];
+    const float2 x = p.part_l[slot(i)];
+    const float l2 = (x.x - base) + x.y;
     const float w = exp2f(l2 - ref);
     sum += w;
     if (l2 != -INFINITY) acc += w * p.part_o[slot(i) * D + d];
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p
   const int64_t at = static_cast<int64_t>(row0 + r) * p.n_h + kvh * p.G + h0 + (n - r * heads);
   const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
   p.out[at * D + d] = *reinterpret_cast<const dsa_bf16*>(&y);
-  if (d == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+  if (d == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (base + (ref + log2f(sum))) * kLn2;
 }
 
 // How a call is cut into units, and what it needs.
@@ -897,7 +903,7 @@ Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n
   pl.merge = !pl.aligned && pl.grid > 1;
   if (pl.merge) {
     pl.o_bytes = static_cast<size_t>(2 * kMaxCtas) * pl.NH * kv->D * 4;
-    pl.l_bytes = static_cast<size_t>(2 * kMaxCtas) * pl.NH * 4;
+    pl.l_bytes = static_cast<size_t>(2 * kMaxCtas) * pl.NH * 8;
     pl.meta_bytes = static_cast<size_t>((pl.units + 1) / 2) * 16;
   }
   return pl;
@@ -1000,7 +1006,7 @@ dsa_status dsa_paged_attn(const dsa_bf16* q, int n_h, const dsa_paged_kv* kv, co
     p.aligned = pl.aligned; p.scale_log2 = scale * kLog2e; p.out = out; p.lse = lse; p.err = err;
     if (pl.merge) {
       p.part_o = reinterpret_cast<float*>(w);
-      p.part_l = reinterpret_cast<float*>(w + pl.o_bytes);
+      p.part_l = reinterpret_cast<float2*>(w + pl.o_bytes);
       p.meta = reinterpret_cast<int2*>(w + pl.o_bytes + pl.l_bytes);
     }
     e = kv->D == 64 ? (f8 ? launch_attn<64, true>(mk, mv, p, pl, s) : launch_attn<64, false>(mk, mv, p, pl, s))

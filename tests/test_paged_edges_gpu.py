@@ -292,3 +292,17 @@ def test_lists_much_longer_than_the_rows(dsa, page, n_sel, starts, fmt):  # noqa
             sel[b, h, :len(pick)] = pick
     for shift in (0, 3):  # (also with holes before the entries)
         _attend(dsa, kv, mirror, batch, table, q_lens, starts, _bf16(g, 4, 8, 64, std=1.5), 0.125, sel=sel.roll(shift, 2))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D,page,q_lens,starts", [(64, 64, [1, 1], [3000, 400]), (128, 32, [3], [3000]), (128, 16, [1], [300])])
+@pytest.mark.parametrize("times,scale", [(1.0, 64.0), (2.0 ** 10, 2.0 ** 9), (2.0 ** 10, 2.0 ** 40), (1.0, 1e30)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_few_rows_with_scores_past_the_f32_fraction(dsa, times, scale, listed, D, page, q_lens, starts, fmt):  # noqa: F811
+    kv, mirror, batch, table, q = _equal_far_keys(dsa, q_lens, starts, D, page, fmt, times, 54)
+    sel = None
+    if listed:
+        vis = min(s // page + 1 for s in starts)
+        sel = torch.stack([torch.randperm(vis, generator=_gen(r))[:vis // 2 + 1] for r in range(2 * sum(q_lens))])
+        sel = sel.view(sum(q_lens), 2, -1).int().contiguous()
+    _check_one_hot(dsa, kv, mirror, batch, table, q_lens, starts, q, scale, sel=sel)
