@@ -247,7 +247,8 @@ struct Cfg {
   static constexpr int kRing = (kCtasPerSm == 3 ? 64 : kCtasPerSm == 2 ? 96 : 176) * 1024 / kEntry;  // entries: K, V, K, V, ...
   static constexpr int kMetas = kRing / 2 + 3;  // a slot is rewritten only after the PV of its tile
   static constexpr int kMetaBytes = kMetas * 8 * 16;
-  static constexpr int kWm = kGroups * 2 * 4 * (kHG + 4);
+  static constexpr int kWmRow = F8 ? 2 * kHG : kHG;  // a warp's maxima of a tile: scores, what the V scales add
+  static constexpr int kWm = kGroups * 2 * 4 * kWmRow;
   static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
   static constexpr int kSmem = 1024 + kRing * kEntry + kQBytes + 2 * kPBytes + kMetaBytes + kWm * 4 + 2 * NH * 4 +
                                4 * NH * 4 + kEpiWarps * 4 * kHG * 4 + 8 * (2 * kRing + kMetas + 8) + 64;
@@ -282,7 +283,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   uint8_t* q_smem = ring + kRing * C::kEntry;
   uint8_t* p_smem = q_smem + C::kQBytes;
   int4* meta = reinterpret_cast<int4*>(p_smem + 2 * C::kPBytes);  // [kMetas][8] position, K scale, V scale
-  float* wm = reinterpret_cast<float*>(meta + kMetas * 8);        // [group][2][4 warps][HG + 4]
+  float* wm = reinterpret_cast<float*>(meta + kMetas * 8);        // [group][2][4 warps][kWmRow]
   float* cq = wm + C::kWm;                                        // [2][NH] factor of a head's scores
   float* lsum = cq + 2 * NH;                                      // [4 warps][NH]
   float* bcast = lsum + 4 * NH;                                   // [warps][4][HG]
@@ -452,7 +453,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int grp = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const int gh = grp * HG;  // first head of the group
-    float* wmg = wm + grp * 2 * 4 * (HG + 4);
+    float* wmg = wm + grp * 2 * 4 * C::kWmRow;
     float* bc = bcast + warp * 4 * HG;  // per warp: references, weight factors, factors of the sums and of O
     int it = 0, seg = 0;
     bool ok = true;
@@ -549,7 +550,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const int pos = mt.x + (key & (p.page - 1)), past = pos - cur.t0;
         float x[HG];
         float lvs = 0.f;
-        if constexpr (F8) lvs = __log2f(warp_max_f32(vs));
+        if constexpr (F8) lvs = __log2f(p.page == 16 ? vs : warp_max_f32(vs));  // (a warp's keys lie in one page, or in two of 16)
         ok = ok && mbar_wait(&s_full[buf], (it >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
@@ -577,7 +578,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         }
         // ---- the tile's maximum per head, over the four warps
         {
-          float* w = wmg + (buf * 4 + wq) * (HG + 4);
+          float* w = wmg + (buf * 4 + wq) * C::kWmRow;
           float r[HG];
 #pragma unroll
           for (int h = 0; h < HG; ++h) r[h] = warp_max_f32(x[h]);
@@ -586,20 +587,28 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             for (int h = 0; h < HG; h += 4) *reinterpret_cast<float4*>(w + h) = make_float4(r[h], r[h + 1], r[h + 2], r[h + 3]);
             if (F8) w[HG] = lvs;
           }
+          if (F8 && p.page == 16) {  // per head: a page below the top score may weigh more
+#pragma unroll
+            for (int h = 0; h < HG; ++h) r[h] = warp_max_f32((x[h] - r[h]) + lvs);
+            if (lane == 0) {
+#pragma unroll
+              for (int h = 0; h < HG; h += 4) *reinterpret_cast<float4*>(w + HG + h) = make_float4(r[h], r[h + 1], r[h + 2], r[h + 3]);
+            }
+          }
         }
         if (!named_bar_and(1 + grp, 128, ok)) { ok = false; break; }
         bool grew, grew_l;
         {
-          const float* w = wmg + buf * 4 * (HG + 4);
+          const float* w = wmg + buf * 4 * C::kWmRow;
           const int h = lane % HG;
           float t = -INFINITY, tp = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) t = fmaxf(t, w[q * (HG + 4) + h]);
+          for (int q = 0; q < 4; ++q) t = fmaxf(t, w[q * C::kWmRow + h]);
           const float mn = fmaxf(m, ceilf(t));
           const float mu = mn == -INFINITY ? 0.f : mn;
           if (F8) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tp = fmaxf(tp, (w[q * (HG + 4) + h] - mu) + w[q * (HG + 4) + HG]);
+            for (int q = 0; q < 4; ++q) tp = fmaxf(tp, (w[q * C::kWmRow + h] - mu) + w[q * C::kWmRow + HG + (p.page == 16 ? h : 0)]);
           }
           const float was = mr + (m - mu), pr = F8 ? fmaxf(was, ceilf(tp)) : 0.f;
           grew_l = __any_sync(0xffffffffu, mn > m);

@@ -306,3 +306,46 @@ def test_few_rows_with_scores_past_the_f32_fraction(dsa, times, scale, listed, D
         sel = torch.stack([torch.randperm(vis, generator=_gen(r))[:vis // 2 + 1] for r in range(2 * sum(q_lens))])
         sel = sel.view(sum(q_lens), 2, -1).int().contiguous()
     _check_one_hot(dsa, kv, mirror, batch, table, q_lens, starts, q, scale, sel=sel)
+
+
+def _tight(q, K, V, seen, scale, vs):
+    """The numerics that the header states, term by term: scores as f32 sums of D
+    products and their scaling (delta), each weight within 2^-8 of itself, for
+    an 8-bit cache (vs not all 1) also within 2^-14 of the largest weight x V
+    scale of its 128 keys, f32 sums over the keys, one rounding of the output to
+    bf16 (2^-8)."""
+    idx = torch.nonzero(seen).flatten()
+    n, D = int(idx.numel()), q.numel()
+    e = torch.full((K.shape[0],), -math.inf, dtype=torch.float64)
+    e[idx] = scale * (K[idx] @ q)
+    lse = float(torch.logsumexp(e, 0))
+    p = torch.exp(e - lse)[:, None]
+    v = torch.where(seen[:, None], V, torch.zeros_like(V))
+    out = (p * v).sum(0)
+    delta = scale * float((K[idx].abs() @ q.abs()).max()) * (D + 8) * 2.0 ** -24
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -8 + 2 * delta + (n + 16) * 2.0 ** -24) * (p * v.abs()).sum(0)
+    if not bool((vs == 1.0).all()):
+        scales = torch.where(seen, vs, torch.zeros_like(vs))
+        pad = -p.shape[0] % 128
+        top = torch.nn.functional.pad(p[:, 0] * scales, (0, pad)).view(-1, 128).max(1).values.repeat_interleave(128)[:p.shape[0]]
+        codes = torch.where(scales[:, None] > 0, v / vs[:, None], torch.zeros_like(v))
+        tol = tol + 2.0 ** -14 * (top[:, None] * codes.abs()).sum(0)
+    return out, lse, tol + 1e-37, delta + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * (1 + abs(lse))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("lq,gap", [(1, 20.8), (3, 20.8), (1, 12.0)])
+def test_the_largest_score_in_a_page_of_tiny_values(dsa, lq, gap, page):  # noqa: F811
+    # pages alternate between V scales of about 2^-25 with scores near 0 and of
+    # about 1 with scores `gap` (natural log) lower; both weigh on the output
+    D = 64
+
+    def hook(k, v):
+        odd = ((torch.arange(k.shape[0]) // page) % 2).bool()
+        k.mul_(0.05)
+        k[..., 0] = torch.where(odd, -gap / 2, 0.0)[:, None].to(k.dtype)
+        v.mul_(torch.where(odd, 1.0, 2.0 ** -25)[:, None, None].to(v.dtype))
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [700], 2, D, page, "e4m3", 71, hook=hook)
+    q = _bf16(g, lq, 8, D, std=0.05)
+    q[..., 0] = 2.0
+    _attend(dsa, kv, mirror, batch, table, [lq], [700], q, 1.0, tol=_tight)
