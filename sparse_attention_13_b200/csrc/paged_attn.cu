@@ -23,6 +23,12 @@ namespace {
 constexpr int kTile = 128;         // keys per tile
 constexpr int kMaxCtas = 480;      // CTAs that may leave partial results
 constexpr int kNoPage = 1 << 30;   // position of a slot that no page holds
+// Weights over 8-bit pages are scaled to at most 256 and held in steps of 2^-14
+// (two E4M3 terms).  The reference follows a tile whose largest weight is more
+// than kFall octaves below it, so that many small weights behind a large one
+// are not lost: no weight is off by more than 2^-14 of its tile's largest.  It
+// stays within kFallMost octaves of the row's largest (O grows as it falls).
+constexpr float kFall = 8.f, kFallMost = 40.f, kLowest = -110.f;  // (2^-118 is a factor of the output)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct PattnParams {
@@ -531,8 +537,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (more) fetch_q(s);
       // lane h (mod HG) keeps the reference exponents of head h: m of the
       // weights, m + mr of the weighted V scales (relative, because a large m
-      // would swallow a scale's share); every thread its keys' sums
-      float m = -INFINITY, mr = -INFINITY, l[HG];
+      // would swallow a scale's share), m + low the lowest that the latter may
+      // fall to; every thread its keys' sums
+      float m = -INFINITY, mr = -INFINITY, low = kLowest, l[HG];
 #pragma unroll
       for (int h = 0; h < HG; ++h) l[h] = 0.f;
       const int heads = min(p.Gx, p.G - cur.h0);
@@ -610,15 +617,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int q = 0; q < 4; ++q) tp = fmaxf(tp, (w[q * C::kWmRow + h] - mu) + w[q * C::kWmRow + HG + (p.page == 16 ? h : 0)]);
           }
-          const float was = mr + (m - mu), pr = F8 ? fmaxf(was, ceilf(tp)) : 0.f;
+          const float was = mr + (m - mu);
+          float pr = 0.f;
+          if (F8) {
+            tp = ceilf(tp);
+            pr = tp > was || (tp < was - kFall && tp > low) ? tp : was;
+          }
           grew_l = __any_sync(0xffffffffu, mn > m);
-          grew = F8 ? __any_sync(0xffffffffu, pr > was) : grew_l;
+          grew = F8 ? __any_sync(0xffffffffu, pr != was) : grew_l;
           if (lane < HG) {
             bc[lane] = mu;
             if (F8) bc[HG + lane] = ex2_approx(pr == -INFINITY ? 8.f : fminf(8.f - pr, 120.f));
             if (grew_l) bc[2 * HG + lane] = mn > m ? ex2_approx(m - mn) : 1.f;
-            if (F8 && grew) bc[3 * HG + lane] = pr > was ? ex2_approx(was - pr) : 1.f;
+            if (F8 && grew) bc[3 * HG + lane] = pr != was ? ex2_approx(was - pr) : 1.f;
           }
+          if (F8) low = fmaxf(fmaxf(low + (m - mu), tp - kFallMost), kLowest);
           m = mn;
           mr = pr;
           __syncwarp();
@@ -639,7 +652,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           for (int e = 0; e < 2; ++e) {
             w[e] = ex2_approx(x[h + e] - bc[h + e]);
             l[h + e] += w[e];
-            if constexpr (F8) w[e] *= vs * bc[HG + h + e];
+            if constexpr (F8) w[e] = w[e] * vs * bc[HG + h + e];  // (in this order no product overflows)
           }
           if constexpr (F8) {
             const uint32_t hi = e4m3x2(w[0], w[1]);

@@ -253,6 +253,8 @@ def _attend(dsa, kv, mirror, batch, table, q_lens, starts, q, scale, sel=None, r
     out, lse, r = out.cpu().double(), lse.cpu().double(), 0
     for b, n in enumerate(q_lens):
         for h in range(n_kv if n else 0):
+            if rows is not None and not any(r + i in rows for i in range(n)):
+                continue
             K, V = mirror.rows(table[b], h)
             vs = mirror.vs[torch.tensor(table[b], dtype=torch.long), h].repeat_interleave(page)
             for i in range(n):
@@ -312,8 +314,8 @@ def _tight(q, K, V, seen, scale, vs):
     """The numerics that the header states, term by term: scores as f32 sums of D
     products and their scaling (delta), each weight within 2^-8 of itself, for
     an 8-bit cache (vs not all 1) also within 2^-14 of the largest weight x V
-    scale of its 128 keys, f32 sums over the keys, one rounding of the output to
-    bf16 (2^-8)."""
+    scale of its 128 keys and 2^-32 of the row's, f32 sums over the keys, one
+    rounding of the output to bf16 (2^-8)."""
     idx = torch.nonzero(seen).flatten()
     n, D = int(idx.numel()), q.numel()
     e = torch.full((K.shape[0],), -math.inf, dtype=torch.float64)
@@ -329,7 +331,9 @@ def _tight(q, K, V, seen, scale, vs):
         pad = -p.shape[0] % 128
         top = torch.nn.functional.pad(p[:, 0] * scales, (0, pad)).view(-1, 128).max(1).values.repeat_interleave(128)[:p.shape[0]]
         codes = torch.where(scales[:, None] > 0, v / vs[:, None], torch.zeros_like(v))
-        tol = tol + 2.0 ** -14 * (top[:, None] * codes.abs()).sum(0)
+        # (rounding to the nearest step is never off by more than the weight itself)
+        off = torch.minimum(p[:, 0] * scales, 2.0 ** -14 * top + 2.0 ** -32 * top.max())
+        tol = tol + (off[:, None] * codes.abs()).sum(0)
     return out, lse, tol + 1e-37, delta + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * (1 + abs(lse))
 
 
@@ -349,3 +353,51 @@ def test_the_largest_score_in_a_page_of_tiny_values(dsa, lq, gap, page):  # noqa
     q = _bf16(g, lq, 8, D, std=0.05)
     q[..., 0] = 2.0
     _attend(dsa, kv, mirror, batch, table, [lq], [700], q, 1.0, tol=_tight)
+
+
+def _copies(dsa, batch, table, q_lens, starts, times):
+    """The batch of one sequence, `times` times over the same pages: so many
+    that no sequence's keys are split between CTAs."""
+    t = batch.block_table.repeat(times, 1).contiguous()
+    return dsa.PagedBatch.from_lens(q_lens * times, starts * times, t), table * times, q_lens * times, starts * times
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("gap", [10.0, 16.0, 17.0, 19.0])
+@pytest.mark.parametrize("lq,page,listed", [(1, 64, False), (3, 16, False), (1, 128, True)])
+def test_many_small_weights_behind_a_large_one(dsa, lq, page, listed, gap, fmt):  # noqa: F811
+    # one token of tiny value draws each row (an attention sink), the others lie
+    # `gap` (natural log) lower: together they decide the output
+    n = 60000
+
+    def hook(k, v):
+        k.mul_(0.25)
+        k[..., 0] = -gap
+        k[5, :, 0] = 0.0
+        v.copy_((v.float().abs() + 0.25).to(v.dtype))
+        v[5] *= 2.0 ** -9
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [n], 1, 64, page, fmt, 81, hook=hook)
+    batch, table, q_lens, starts = _copies(dsa, batch, table, [lq], [n], 320)
+    q = _bf16(g, 320 * lq, 4, 64, std=0.125)
+    q[..., 0] = 1.0
+    sel = torch.arange(-(-(n + lq) // page), dtype=torch.int32).expand(320 * lq, 1, -1).contiguous() if listed else None
+    _attend(dsa, kv, mirror, batch, table, q_lens, starts, q, 1.0, sel=sel, rows={0, lq - 1, 320 * lq - 1}, tol=_tight)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq,page", [(1, 16), (2, 128), (12, 64)])
+@pytest.mark.parametrize("depth", [6.0, 14.0, 60.0])
+@pytest.mark.parametrize("times", [1, 160])
+def test_references_that_rise_and_fall(dsa, times, depth, lq, page, fmt):  # noqa: F811
+    # runs of 128 keys whose scores go down and up again by `depth`, with values
+    # that grow where the weights shrink
+    def hook(k, v):
+        run = (torch.arange(k.shape[0]) // 128 * 5 % 7).float() / 6  # 0 .. 1
+        k.mul_(0.25)
+        k[..., 0] = (-depth * run)[:, None].to(k.dtype)
+        v.mul_((2.0 ** (depth * run * 1.25).round())[:, None, None].to(v.dtype))
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [4000], 2, 128, page, fmt, 82, hook=hook)
+    batch, table, q_lens, starts = _copies(dsa, batch, table, [lq], [4000], times)
+    q = _bf16(g, times * lq, 8, 128, std=0.125)
+    q[..., 0] = 1.0
+    _attend(dsa, kv, mirror, batch, table, q_lens, starts, q, 1.0, rows={0, lq - 1, times * lq - 1}, tol=_tight)
