@@ -373,10 +373,14 @@ dsa_status dsa_page_topk(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
  * head (page numbers within the sequence in any order, no page twice; entries
  * outside the row's visible pages are skipped, as -1 is).  A row that sees
  * nothing gets out = 0 and lse = -inf.
- * Numerics: scores are f32 sums of exact products; the softmax runs in f32;
- * the weights enter the P.V product with at least 8 significant bits (bf16,
- * f16, or two terms of a narrower type), accumulated in f32; out is rounded
- * once.
+ * Numerics: scores are f32 sums of products, exact ones over a bf16 cache; over
+ * an 8-bit cache a query's elements have 8 significant bits down to 2^-15 of the
+ * largest of their row and head and are off by at most 2^-22 of it below.  The
+ * softmax runs in f32.  The weights enter the P.V product with 8 significant
+ * bits (bf16, f16, or two terms of a narrower type); over an 8-bit cache a weight
+ * times its page's V scale may also be off by 2^-14 of the largest of the 128
+ * around it (positions, or entries of the row's list) or 2^-32 of the row's
+ * largest, but by no more than itself.  Sums are f32; out is rounded once.
  *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written; not q
  *   itself); lse [total_q, n_h] f32 (written; may be NULL); 0 < scale <= 1e30.
  * Supported: n_h a multiple of n_kv, n_h <= 128; n_sel <= 1024.

@@ -33,9 +33,15 @@ constexpr int kThreads = 16 * 32;  // four warpgroups, for the register split (t
 // 65,536 registers: 128 a thread at launch; 2 x 128 x 208 + 2 x 128 x 48
 constexpr int kSoftRegs = 208, kOtherRegs = 48;
 // A row's reference exponent may lag its maximum until sixteen weights sum to
-// more than this (f16 holds 2^16): rescaling O is rare, and no maximum is taken
-// on the way.
-constexpr float kMostSum = 4096.f;
+// more than kMostSum: rescaling O is rare, and no maximum is taken on the way.
+// The f16 weights of an 8-bit cache are at most 2^16 and have steps of 2^-24:
+// their reference lies kLift octaves below the maximum, so that weights keep 8
+// bits down to 2^-24 of the row's largest and are off by 2^-33 of it below (many
+// small weights behind a large one count).  The sums are kept in units of the
+// maximum all the same: a V scale of 2^-100 adds its share to them.
+template <bool F8> constexpr float kMostSum = F8 ? 32768.f : 4096.f;
+template <bool F8> constexpr float kLift = F8 ? 8.f : 0.f;
+constexpr float kUnlift = 1.f / 256.f;
 // A score is rounded to f32 before it becomes the reference, but not inside the
 // fused exponent score * k - reference.  Up to this reference the difference is
 // at most 2^-8; beyond, the exponent takes the rounded score as well (at 2^28
@@ -70,7 +76,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 }
 
 // The weights of a row over half a tile, 2^(score * k + add), rounded and packed two
-// to a word in pk; sum: their f32 sum in units of the row's reference; high: the
+// to a word in pk; sum: their f32 sum without the V scales, in units of the reference + kLift; high: the
 // largest sum of sixteen.  GENERAL: columns from lim on are masked, and a V
 // scale so small that it would flush the weights (thin: below vmax by 2^90)
 // does not flush their share of the sum.  The other case has no branches, so
@@ -119,7 +125,7 @@ __device__ __forceinline__ void tile_weights(uint32_t ts, const float4* mt, int 
         part = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) part += e < left ? ex2_approx(fmaf(__uint_as_float(s[e]), k, -mu)) : 0.f;
-        inv = 1.f;
+        inv = kUnlift;
       }
       sum = F8 ? fmaf(part, inv, sum) : sum + part;
     }
@@ -142,7 +148,7 @@ __device__ __forceinline__ void scale_o(uint32_t to, float f) {
 }
 
 // A row's state: reference exponent (ref + off; off is zero up to kFarRef) and
-// the sum of 2^(score - reference).
+// the sum of 2^(score - reference - kLift).
 struct RowState {
   float ref, off, l;
 };
@@ -177,7 +183,7 @@ __device__ __forceinline__ RowState far_half(uint32_t ts, uint32_t to, const flo
   for (int r = 0; r < 4; ++r) {
     load(r, x);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) off = fmaxf(off, __fadd_rn(__fsub_rn(x[e], mu), scales(r).y));
+    for (int e = 0; e < 16; ++e) off = fmaxf(off, __fadd_rn(__fsub_rn(x[e], mu), scales(r).y) - kLift<F8>);
   }
   const float f = off == was ? 1.f : ex2_approx(was - off);
   if (!first && __any_sync(0xffffffffu, f != 1.f)) scale_o<D>(to, f);
@@ -200,7 +206,7 @@ __device__ __forceinline__ RowState far_half(uint32_t ts, uint32_t to, const flo
       }
       pk[e / 2] = F8 ? pack_f16(w[0], w[1]) : pack_bf16(w[0], w[1]);
     }
-    sum = fmaf(part, thin ? 1.f : sc.z, sum);
+    sum = fmaf(part, thin ? kUnlift : sc.z, sum);
     tmem_st32x8(ts + r * 8, pk);
   }
   return {next, off, fmaf(row.l, f, sum)};
@@ -268,7 +274,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
   uint8_t* q_smem = smem;
   uint8_t* ring = q_smem + 2 * C::kEntry;
   uint8_t* stage = ring + kRing * C::kEntry;
-  float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, 1 / V scale, flags
+  float4* meta = reinterpret_cast<float4*>(stage + kStages * C::kStage);  // [kMetas][8] K scale, log2 V scale, kUnlift / V scale, flags
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(meta) + C::kMetaBytes);
   uint64_t *full = bars, *empty = full + kRing, *st_full = empty + kRing, *st_empty = st_full + kStages;
   uint64_t *meta_full = st_empty + kStages;
@@ -380,7 +386,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
           vmax = fmaxf(vmax, warp_max_f32(lv));
           const bool thin = lv < vmax - 90.f;
           const float w = (thin ? 1.f : 0.f) + (__any_sync(0xffffffffu, thin) ? 2.f : 0.f);
-          if (lane < p.ppt) meta[i % kMetas * 8 + lane] = make_float4(mk, lv, __fdividef(1.f, mv), w);
+          if (lane < p.ppt) meta[i % kMetas * 8 + lane] = make_float4(mk, lv, __fdividef(kUnlift, mv), w);
           __syncwarp();
           if (lane == 0) mbar_arrive(&meta_full[i % kMetas]);
         }
@@ -642,7 +648,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
               top = fmaxf(top, part);
             }
           }
-          const float next = fmaxf(ref, top);
+          const float next = fmaxf(ref, top - kLift<F8>);
           far = __any_sync(0xffffffffu, fabsf(next) > kFarRef && next != -INFINITY);
           if (far) break;
           const float f = next == ref ? 1.f : ex2_approx(ref - next);
@@ -659,8 +665,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         float high;
         if (edge || thin) tile_weights<F8, true>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
         else tile_weights<F8, false>(th, mt, p.shift, cr, mu, lim, pk, sum, high);
-        // (once the maxima have been taken no exponent is above 2^-8: one more try at most)
-        if (tries || !__any_sync(0xffffffffu, high > kMostSum)) break;
+        // (once the maxima have been taken no exponent is above kLift + 2^-8: one more try at most)
+        if (tries || !__any_sync(0xffffffffu, high > kMostSum<F8>)) break;
         find = true;
       }
       if (far) {
@@ -684,8 +690,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     ok = __all_sync(0xffffffffu, ok);
     if (ok && q < u.nq) {
       tc_fence_after();
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float ls = off + log2f(l);  // with ref: log2 of the row's sum (apart, since ref may swallow it)
+      const float inv = l == 0.f ? 0.f : (F8 ? kUnlift : 1.f) / l;
+      const float ls = off + kLift<F8> + log2f(l);  // with ref: log2 of the row's sum (apart, since ref may swallow it)
       const int64_t part = ((id * p.splits + split) * 2 + q) * 128 + m;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {

@@ -364,7 +364,7 @@ def _copies(dsa, batch, table, q_lens, starts, times):
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("gap", [10.0, 16.0, 17.0, 19.0])
-@pytest.mark.parametrize("lq,page,listed", [(1, 64, False), (3, 16, False), (1, 128, True)])
+@pytest.mark.parametrize("lq,page,listed", [(1, 64, False), (3, 16, False), (12, 64, False), (1, 128, True)])
 def test_many_small_weights_behind_a_large_one(dsa, lq, page, listed, gap, fmt):  # noqa: F811
     # one token of tiny value draws each row (an attention sink), the others lie
     # `gap` (natural log) lower: together they decide the output
