@@ -440,13 +440,6 @@ __device__ __forceinline__ void pooled_query(const SelParams& p, int64_t row, in
   for (int i = 0; i < kCols; ++i) qc[lane * kCols + i] = fine ? static_cast<int8_t>(__float2int_rn(__fmul_rn(f[i], inv))) : 0;
 }
 
-template <int D>
-__device__ __forceinline__ void load_summary(const PagedArgs& a, int64_t unit, int4 (&s)[D / 16], float& scale) {
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) s[i] = ld_global(reinterpret_cast<const int4*>(a.sum + unit * D) + i);
-  scale = ld_global(a.sum_scale + unit);
-}
-
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 // A key halfway between lo and hi: first by value (float keys crowd around

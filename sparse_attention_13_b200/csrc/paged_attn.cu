@@ -36,7 +36,7 @@ struct PattnParams {
   const dsa_bf16* q;
   const int32_t* sel;
   int n_h, G, page, shift, ppt, inclusive, n_sel;  // shift: log2 page; ppt: pages per tile
-  int Gx, R, hbs, max_rb;  // heads and rows of a unit, head blocks, row blocks
+  int Gx, R, hbs, max_rb;  // heads and rows of a unit, head blocks (sparse), row blocks (dense)
   int tpu, aligned;        // sparse: tiles per unit; CTAs take whole units
   float scale_log2;
   dsa_bf16* out;
@@ -75,7 +75,7 @@ struct Walker {
     blocks = (rows + p.R - 1) / p.R;
     // (where CTAs take whole units, a unit counts as one)
     t = rows && !p.aligned ? max(1, (paged_visible(p.a, s, rows - 1, p.inclusive) + kTile - 1) / kTile) : 1;
-    return static_cast<long long>(blocks) * p.a.n_kv * p.hbs * t;
+    return static_cast<long long>(blocks) * p.a.n_kv * t;
   }
 
   __device__ __forceinline__ explicit Walker(const PattnParams& pp) : p(pp) {
@@ -146,8 +146,8 @@ struct Walker {
         const long long u = (pos - base) / tiles;
         tile = static_cast<int>(pos - base - u * tiles);
         at = static_cast<int>(u % nrb);
-        kvh = static_cast<int>(u / nrb) / p.hbs;
-        hb = static_cast<int>(u / nrb) % p.hbs;
+        kvh = static_cast<int>(u / nrb);
+        hb = 0;
       }
     }
   }
@@ -172,7 +172,7 @@ struct Walker {
         weight = seq(++b, r0, n, nrb, tiles);
       }
       nominal = tiles;
-      s.unit = ((b * p.a.n_kv + kvh) * p.hbs + hb) * p.max_rb + at;
+      s.unit = (b * p.a.n_kv + kvh) * p.max_rb + at;
       s.row0 = r0 + at * p.R;
       s.nr = min(p.R, n - at * p.R);
       s.t0 = paged_visible(p.a, b, at * p.R, p.inclusive);
@@ -193,7 +193,7 @@ struct Walker {
       if (++at == (SPARSE ? p.a.total_q : nrb)) {
         at = 0;
         if (SPARSE) b = -1;
-        if (++hb == p.hbs) {
+        if (!SPARSE || ++hb == p.hbs) {
           hb = 0;
           if (++kvh == p.a.n_kv) kvh = 0;
         }
@@ -852,9 +852,8 @@ __global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p
     h0 = rem % p.hbs * p.Gx;
   } else {
     const int rb = unit % p.max_rb;
-    int rem = unit / p.max_rb;
-    h0 = rem % p.hbs * p.Gx;
-    rem /= p.hbs;
+    const int rem = unit / p.max_rb;
+    h0 = 0;
     kvh = rem % p.a.n_kv;
     int r0, rows;
     paged_rows(p.a, rem / p.a.n_kv, r0, rows);
@@ -901,12 +900,14 @@ Plan make_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n
   Plan pl{};
   const int G = n_h / kv->n_kv;
   pl.G = G;
-  // columns of a unit: the group's heads, times a few rows when all pages are read
+  // columns of a unit: the group's heads, times a few rows when all pages are
+  // read (32 columns at most then: use_prefill; selected pages take larger
+  // groups in blocks of 32 heads)
   const long long want = n_sel ? G : static_cast<long long>(G) * pb->max_Lq;
   pl.NH = want <= 8 ? 8 : (want <= 16 ? 16 : 32);
   pl.Gx = std::min(G, pl.NH);
   pl.hbs = (G + pl.Gx - 1) / pl.Gx;
-  pl.R = n_sel || pl.hbs > 1 ? 1 : pl.NH / pl.Gx;
+  pl.R = n_sel ? 1 : pl.NH / pl.Gx;
   pl.max_rb = n_sel ? 1 : (pb->max_Lq + pl.R - 1) / pl.R;
   pl.tpu = n_sel ? (n_sel * kv->page + kTile - 1) / kTile : (pb->max_Lk + kTile - 1) / kTile;
   pl.units = (n_sel ? static_cast<long long>(pb->total_q) : static_cast<long long>(pb->B) * pl.max_rb) * kv->n_kv * pl.hbs;

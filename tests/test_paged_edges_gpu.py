@@ -401,3 +401,53 @@ def test_references_that_rise_and_fall(dsa, times, depth, lq, page, fmt):  # noq
     q = _bf16(g, times * lq, 8, 128, std=0.125)
     q[..., 0] = 1.0
     _attend(dsa, kv, mirror, batch, table, q_lens, starts, q, 1.0, rows={0, lq - 1, times * lq - 1}, tol=_tight)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_h,n_kv,lq,n_sel,start", [(40, 1, 1, 40, 5000), (128, 1, 3, 20, 2000), (66, 2, 5, 3, 700), (128, 2, 1, 300, 300)])
+def test_selected_pages_of_groups_above_32_heads(dsa, n_h, n_kv, lq, n_sel, start, fmt):  # noqa: F811
+    # a group's heads are cut into blocks of 32, with and without a merge
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [start], n_kv, 64, 16, fmt, 91)
+    q = _bf16(g, lq, n_h, 64, std=1.5)
+    sel = torch.full((lq, n_kv, n_sel), -1, dtype=torch.int32)
+    for r in range(lq):
+        for h in range(n_kv):
+            pick = torch.randperm((start + r) // 16 + 1, generator=g)[:n_sel].int()
+            sel[r, h, :len(pick)] = pick
+    _attend(dsa, kv, mirror, batch, table, [lq], [start], q, 0.125, sel=sel)
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (128, 128), (64, 32)])
+@pytest.mark.parametrize("cut", [False, True])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_summaries_bit_for_bit(dsa, fmt, cut, D, page):  # noqa: F811
+    # codes and scales by the header's rule, from the cache's own contents: f32
+    # sums by halving, and each operation rounded
+    g = _gen(92)
+    lens = [3 * page, 2 * page + 5, page - 1]
+    table, t, n_pages = _table(lens, [0] * 3, page, g)
+    kv = _pool(dsa, n_pages, page, 2, D, fmt)
+    k = _bf16(g, sum(lens), 2, D)
+    if cut:  # in three calls, the second of which rescales older codes
+        ks, at = k.split(lens), [0, 0, 0]
+        for i in range(3):
+            n = [len(x) // 3 if i < 2 else len(x) - a for x, a in zip(ks, at)]
+            part = torch.cat([x[a:a + m] * (1 + 3 * i) for x, a, m in zip(ks, at, n)])
+            dsa.paged_append(kv, dsa.PagedBatch.from_lens(n, at, t), part.cuda(), part.cuda())
+            at = [a + m for a, m in zip(at, n)]
+    else:
+        dsa.paged_append(kv, dsa.PagedBatch.from_lens(lens, [0] * 3, t), k.cuda(), k.cuda())
+    for b, n in enumerate(lens):
+        for j in range(n // page):
+            pg = table[b][j]
+            for h in range(2):
+                x = kv.k[pg, h].cpu().float()
+                while x.shape[0] > 1:
+                    half = x.shape[0] // 2
+                    x = x[:half] + x[half:]
+                x = x[0] * (kv.k_scale[pg, h].cpu() if fmt == "e4m3" else 1.0)
+                top = x.abs().max()
+                codes = (x * (top.reciprocal() * 127.0)).round().to(torch.int8)
+                assert torch.equal(kv.sum[pg, h].cpu(), codes)
+                assert kv.sum_scale[pg, h].item() == ((top * torch.tensor(1 / 127, dtype=torch.float32)) / page).item()
+    assert torch.isnan(kv.sum_scale[table[2][0]]).all()  # (an incomplete page has none)
