@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(D) paged_attn_merge_kernel(const PattnParams p
   const int heads = min(p.Gx, p.G - h0);
   if (nr <= 0 || n >= heads * nr) return;
   const int2 c = p.meta[unit];
-  if (c.x < 0) return;
+  if (c.x < 0 || c.x >= kMaxCtas || c.y >= kMaxCtas) return;  // (anything may stand here after a call that gave up waiting)
   const auto slot = [&](int i) { return static_cast<int64_t>(2 * i + (i == c.x)) * NH + n; };
   float base = -INFINITY, top = -INFINITY;  // top relative to the largest x, since that may swallow y
   for (int i = c.x; i <= c.y; ++i) {
