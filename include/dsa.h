@@ -271,7 +271,8 @@ dsa_status dsa_mx_quantize(const dsa_bf16 *x, int64_t rows, int cols, int fmt,
  *     summary for each COMPLETE page: sum * sum_scale is the mean of the
  *     page's cached keys rounded to whole steps of amax / 127.  Both NULL when
  *     no page selection is used.
- * Supported: page in {16, 32, 64, 128}; D in {64, 128}; n_pages * n_kv < 2^31.
+ * Supported: page in {16, 32, 64, 128}; D in {64, 128}; n_kv <= 128; n_pages *
+ * n_kv < 2^31.
  *
  * A batch holds B sequences with packed rows as in dsa_varlen: rows cu_q[b] ..
  * cu_q[b+1]-1 belong to sequence b, and row i of it is the token at position
@@ -279,7 +280,8 @@ dsa_status dsa_mx_quantize(const dsa_bf16 *x, int64_t rows, int cols, int fmt,
  * page of a sequence: positions j * page .. j * page + page - 1 of sequence b
  * are in block_table[b * max_pages + j].  cu_q, start_pos and block_table are
  * DEVICE int32 arrays; total_q = cu_q[B] and the bounds max_Lq >= every row
- * count and max_Lk >= every start_pos[b] + rows size the launches.
+ * count (at most total_q) and max_Lk >= every start_pos[b] + rows (at most 2^30
+ * and max_pages * page) size the launches.
  *
  * Contract, checked on the device by dsa_check_paged: cu_q starts at 0, never
  * decreases and ends at total_q; start_pos[b] >= 0; the bounds hold; the table
@@ -337,7 +339,7 @@ typedef struct {
  * completes, from the cached (rounded) keys: their sum over the slots by
  * halving (slot i + slot i + page/2, ...) in f32, codes rint(sum * (127 * (1 /
  * amax))), scale (amax * (1 / 127)) / page, each operation rounded to f32; a page whose sum is not finite, or
- * below 3.8e-37 everywhere, gets zeros. */
+ * below 3.8e-37 everywhere, gets zeros.  Supported: n_h <= 1024. */
 dsa_status dsa_paged_append(const dsa_paged_kv *kv, const dsa_paged_batch *batch,
                             const dsa_bf16 *k, int64_t k_row_stride, const dsa_bf16 *v,
                             int64_t v_row_stride, const float *cos, const float *sin,
