@@ -697,7 +697,7 @@ __device__ __forceinline__ void mma_s8_16x8x32(int (&d)[4], uint32_t a0, uint32_
 // warp selects for each row from the scores in shared memory (forced pages:
 // +inf).  Bound by instruction issue: about 1,700 per warp and row at 1,000
 // pages, a third of them the scores (4,096 rows x 4 heads, 960 pages on
-// average: 66 us; with dot products on the CUDA cores and halving it took 117).
+// average: 68 us; with dot products on the CUDA cores and halving it took 117).
 constexpr int kSelRows = 8, kRowBins = 256;
 template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_topk_rows_kernel(const SelParams p) {

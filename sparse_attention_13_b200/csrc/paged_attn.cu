@@ -9,8 +9,9 @@
 //     O^T[D, N]       += V^T . P        A = V tile (MN-major), B = P rows
 // An 8-bit cache is never widened.  E4M3 x E4M3 products are exact, and the
 // 16-bit operands are split into two E4M3 terms, x = hi + lo / 32, which hold
-// the 8 significant bits of a bf16 value exactly: the columns are the heads'
-// hi terms, then their lo terms, with an accumulator each (N = 2 heads).
+// the 8 significant bits of a bf16 value down to 2^-15 of the largest (256), and
+// steps of 2^-14 below: the columns are the heads' hi terms, then their lo
+// terms, with an accumulator each (N = 2 heads).
 #include <algorithm>
 #include <string>
 
@@ -229,8 +230,9 @@ struct Walker {
 template <int D, bool F8, int NH, bool SPARSE>
 struct Cfg {
   // Heads per epilogue group of four warps.  Four groups of 8 for 32 heads of an
-  // 8-bit cache (177 us against 194 for two of 16, 16 x 30,000 tokens x 4 heads);
-  // a bf16 cache, with half the work per weight, loses by it (162 against 157).
+  // 8-bit cache (177 us against 194 for two of 16, 16 x 30,000 tokens x 4 heads,
+  // before the references fell with the tiles; 183 since); a bf16 cache, with
+  // half the work per weight, loses by it (162 against 157).
   static constexpr int kHG = NH < 16 || (F8 && NH == 32) ? 8 : 16;
   static constexpr int kGroups = NH / kHG;
   static constexpr int kEpiWarps = 4 * kGroups;
@@ -272,11 +274,11 @@ __device__ __forceinline__ uint32_t op_off(int n, int c) {
 // Warps 0 .. 4 groups - 1: softmax and output (thread = key in the scores,
 // = column of D in the output); then one TMA warp and one MMA warp.  Bound by
 // the cache's bytes for decode: the ring keeps 96 KB per CTA in flight (8
-// sequences x 200,000 8-bit tokens x 8 heads of 128: 430 to 450 us, 6.3 to 6.5
-// TB/s; 32 ragged sequences of up to 16,384 bf16 tokens x 4 heads: 131 us, 6.2
-// TB/s).  Bound by L2 where every row reads pages of its own (2,048 rows x 8
-// heads x 32 pages of 64: 1,041 us, 8.2 TB/s), and by the softmax warps' chain
-// (about 2,700 cycles a tile) where a tile has few bytes or many heads.
+// sequences x 200,000 8-bit tokens x 8 heads of 128: 440 to 455 us, 6.2 to 6.4
+// TB/s; 32 ragged sequences of up to 16,384 bf16 tokens x 4 heads: 130 to 133 us,
+// 6.1 to 6.3 TB/s).  Bound by L2 where every row reads pages of its own (2,048
+// rows x 8 heads x 32 pages of 64: 1,057 us, 8.1 TB/s), and by the softmax warps'
+// chain (about 2,700 cycles a tile) where a tile has few bytes or many heads.
 template <int D, bool F8, int NH, bool SPARSE>
 __global__ void __launch_bounds__(Cfg<D, F8, NH, SPARSE>::kThreads, Cfg<D, F8, NH, SPARSE>::kCtasPerSm)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -952,7 +954,13 @@ cudaError_t launch_attn(const CUtensorMap& k, const CUtensorMap& v, const PattnP
                     : (pl.NH == 16 ? launch_attn<D, F8, 16>(k, v, p, pl, s) : launch_attn<D, F8, 32>(k, v, p, pl, s));
 }
 
-// Many rows that read all pages: query rows on the tile's rows.
+// Many rows that read all pages: query rows on the tile's rows.  The border is
+// the most columns of the other kernel.  At 40, 64 and 128 columns (5, 8 and 16
+// rows x 8 heads) that one, in several units, takes 156, 193 and 274 us against
+// 194, 195 and 355 here for 16 sequences of up to 30,000 bf16 tokens (8-bit 182,
+// 223 and 377 against 246, 248 and 455), but 42, 47 and 72 against 35, 35 and 36
+// for 32 sequences of up to 2,000 (8-bit 46, 52 and 82 against 40, 42 and 44);
+// for one sequence the two are equal.
 bool use_prefill(const dsa_paged_kv* kv, const dsa_paged_batch* pb, int n_h, int n_sel) {
   return !n_sel && static_cast<long long>(n_h / kv->n_kv) * pb->max_Lq > 32;
 }

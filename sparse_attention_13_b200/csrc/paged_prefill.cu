@@ -8,14 +8,16 @@
 // S and O live in TMEM (all 512 columns); P overwrites S and is the A operand
 // of the second product.  An 8-bit cache is widened to f16 (exact) on its way
 // from a staging tile to the operand tile by four warps of their own; Q rows
-// are scaled to f16 by a power of two per row, so that the products stay exact.
+// are scaled to f16 by a power of two per row: exact down to 2^-16 of the row's
+// largest element, off by 2^-25 of it below.
 //
 // Bound by the softmax warps: 128 x 128 exponentials a tile are 1,024 cycles of
 // the special-function unit, as long as the tile's two products, and the
 // instructions around them take as long again.  4,096 rows x 64 heads at 16,384
-// 8-bit tokens (heads of 128): 2.0 ms, 950 TFLOP/s, 59% of the measured cuBLAS
-// rate.  Moving every fourth exponential to a polynomial made it slower (2.15
-// ms), as did polling instead of sleeping in the softmax warps (2.05 ms).
+// 8-bit tokens (heads of 128): 2.09 to 2.12 ms, 910 to 920 TFLOP/s, 57% of the
+// measured cuBLAS rate.  When that was 2.0 ms, moving every fourth exponential to
+// a polynomial made it slower (2.15 ms), as did polling instead of sleeping in
+// the softmax warps (2.05 ms).
 #include <algorithm>
 
 #include "paged.cuh"
@@ -797,6 +799,10 @@ PrefillPlan paged_prefill_plan(const dsa_paged_kv* kv, const dsa_paged_batch* pb
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
   const int tiles = (pb->max_Lk + kTile - 1) / kTile;
+  // Few units share the GPU in equal parts of their keys, of three tiles and more
+  // (64 rows x 8 heads x 4 groups at up to 2,000 tokens: 28.2 us, in parts of one
+  // tile 30.2, of eight 33.3; 8-bit 35.5, 36.1 and 42.5; at 500 and at 30,000
+  // tokens, and with more rows, all three are equal).
   pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / units, tiles / 3)));
   if (pl.splits > 1) {
     pl.o_bytes = static_cast<size_t>(units) * pl.splits * 256 * kv->D * 4;
