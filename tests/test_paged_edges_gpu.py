@@ -338,7 +338,7 @@ def _tight(q, K, V, seen, scale, vs):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64])
-@pytest.mark.parametrize("lq,gap", [(1, 20.8), (3, 20.8), (1, 12.0)])
+@pytest.mark.parametrize("lq,gap", [(1, 20.8), (3, 20.8), (1, 12.0), (40, 20.8), (40, 12.0)])
 def test_the_largest_score_in_a_page_of_tiny_values(dsa, lq, gap, page):  # noqa: F811
     # pages alternate between V scales of about 2^-25 with scores near 0 and of
     # about 1 with scores `gap` (natural log) lower; both weigh on the output
@@ -451,3 +451,21 @@ def test_summaries_bit_for_bit(dsa, fmt, cut, D, page):  # noqa: F811
                 assert torch.equal(kv.sum[pg, h].cpu(), codes)
                 assert kv.sum_scale[pg, h].item() == ((top * torch.tensor(1 / 127, dtype=torch.float32)) / page).item()
     assert torch.isnan(kv.sum_scale[table[2][0]]).all()  # (an incomplete page has none)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("lq", [1, 3, 40])
+@pytest.mark.parametrize("gap", [0.0, 30.0, 55.0, 75.0])
+@pytest.mark.parametrize("tiny_first", [False, True])
+def test_scales_a_hundred_octaves_apart(dsa, tiny_first, gap, lq, page):  # noqa: F811
+    # pages alternate between V scales of about 2^-100 and of about 2; those with
+    # tiny values have scores `gap` (natural log) higher, and so the softmax's mass
+    def hook(k, v):
+        big = ((torch.arange(k.shape[0]) // page) % 2 == int(tiny_first))
+        k.mul_(0.05)
+        k[..., 0] = torch.where(big, -gap / 2, 0.0)[:, None].to(k.dtype)
+        v.mul_(torch.where(big, 512.0, 2.0 ** -93)[:, None, None].to(v.dtype))
+    kv, mirror, batch, table, g = _filled(dsa, [lq], [900], 2, 64, page, "e4m3", 73, hook=hook)
+    q = _bf16(g, lq, 8, 64, std=0.05)
+    q[..., 0] = 2.0
+    _attend(dsa, kv, mirror, batch, table, [lq], [900], q, 1.0, tol=_tight)
