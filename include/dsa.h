@@ -382,7 +382,8 @@ dsa_status dsa_page_topk(const dsa_bf16 *q, int n_h, const dsa_paged_kv *kv,
  * bits (bf16, f16, or two terms of a narrower type); over an 8-bit cache a weight
  * times its page's V scale may also be off by 2^-14 of the largest of the 128
  * around it (positions, or entries of the row's list) or 2^-32 of the row's
- * largest (2^-22 where its scale is below 2^-70), but by no more than itself.  Sums are f32; out is rounded once.
+ * largest (2^-22 where its scale is below 2^-70), but by no more than itself.
+ * Sums are f32; out is rounded once.
  *   q [total_q, n_h, D] bf16; out [total_q, n_h, D] bf16 (written; not q
  *   itself); lse [total_q, n_h] f32 (written; may be NULL); 0 < scale <= 1e30.
  * Supported: n_h a multiple of n_kv, n_h <= 128; n_sel <= 1024.
